@@ -77,6 +77,25 @@ SIGNATURES = {
     "bitlinear_forward_blocks": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "bitlinear_pack_weights_blocks_bf16": (ctypes.c_int, [_VP, _I64, _I64, _VP, _VP, _VP, _SZ, _VP]),
     "bitlinear_forward_blocks_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "bitlinear_w4_groups": (_I64, [_I64, ctypes.c_int]),
+    "bitlinear_w4_packed_bytes": (_SZ, [_I64, _I64, ctypes.c_int, ctypes.c_int]),
+    "bitlinear_pack_weights_w4": (ctypes.c_int, [_VP, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _SZ, _VP]),
+    "bitlinear_pack_weights_w4_bf16": (ctypes.c_int, [_VP, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _SZ,
+                                                      _VP]),
+    "bitlinear_w4_import": (ctypes.c_int, [_VP, _VP, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP]),
+    "bitlinear_w4_export": (ctypes.c_int, [_VP, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP]),
+    "bitlinear_w4_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "bitlinear_forward_w4": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP, _SZ,
+                                            _VP]),
+    "bitlinear_forward_w4_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP,
+                                                 _SZ, _VP]),
+    "bitlinear_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    "bitlinear_sample_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    "bitlinear_w4_sample_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "bitlinear_forward_w4_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP,
+                                                   _VP, _VP, _VP, _SZ, _VP]),
+    "bitlinear_forward_w4_sample_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP,
+                                                        _VP, _VP, _VP, _VP, _SZ, _VP]),
     "bitlinear_workspace_error": (ctypes.c_int, [_VP, _SZ, _VP]),
     "bitlinear_selftest_wait_timeout": (ctypes.c_int, [_VP, _SZ, ctypes.c_uint64, _VP]),
     "bitlinear_forward_noalloc": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP]),
@@ -102,10 +121,27 @@ class LinearCall(ctypes.Structure):
     ]
 
 
+class Sampling(ctypes.Structure):
+    """Mirror of bl_sampling (include/bitlinear.h)."""
+
+    _fields_ = [
+        ("temperature", ctypes.c_void_p),
+        ("top_k", ctypes.c_void_p),
+        ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
+        ("temperature_value", ctypes.c_float),
+        ("top_k_value", ctypes.c_int32),
+        ("top_p_value", ctypes.c_float),
+        ("min_p_value", ctypes.c_float),
+    ]
+
+
 BL_FLAG_STREAM_WEIGHTS_EARLY = 1
 BL_FLAG_ONE_LAUNCH_PER_CALL = 2
 BL_I2S_CONSECUTIVE = 0
 BL_I2S_QUARTERS = 1
+BL_SCALE_F32 = 0
+BL_SCALE_BF16 = 1
 
 
 class BitLinearError(RuntimeError):

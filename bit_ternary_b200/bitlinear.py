@@ -9,6 +9,8 @@ the page read out of bounds).
 """
 from __future__ import annotations
 
+import contextlib
+import ctypes
 from typing import Optional, Tuple
 
 import torch
@@ -33,6 +35,15 @@ __all__ = [
     "pack_weights_blocks",
     "forward_blocks",
     "blocks_workspace_size",
+    "W4Weights",
+    "pack_weights_w4",
+    "import_w4",
+    "unpack_w4",
+    "forward_w4",
+    "w4_workspace_size",
+    "sample",
+    "forward_w4_sample",
+    "w4_sample_workspace_size",
     "workspace_size",
     "workspace_error",
     "BitLinear",
@@ -292,6 +303,212 @@ def forward_blocks(x: torch.Tensor, packed: torch.Tensor, D: torch.Tensor,
     _lib.call(fn, x.data_ptr(), M, N, K, packed.data_ptr(), D.data_ptr(), y.data_ptr(),
               ws.data_ptr(), ws.numel(), _stream_handle(x.device))
     return y
+
+
+_W4_SCALES = {torch.float32: _lib.BL_SCALE_F32, torch.bfloat16: _lib.BL_SCALE_BF16}
+
+
+def _on_device(device: torch.device):
+    """The library launches on the current device: make it the tensors' own."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(t: torch.Tensor, name: str, device: torch.device) -> None:
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+class W4Weights:
+    """A weight [N, K] of 4-bit codes with a scale per `group` columns of a row
+    (scale_dtype fp32 or bf16), in the library's packed layout."""
+
+    def __init__(self, data: torch.Tensor, N: int, K: int, group: int, scale_dtype: torch.dtype):
+        if scale_dtype not in _W4_SCALES:
+            raise TypeError(f"scales must be fp32 or bf16, got {scale_dtype}")
+        need = _w4_packed_bytes(N, K, group, scale_dtype)
+        _need_cuda(data, "data", torch.uint8)
+        if data.numel() != need:
+            raise ValueError(f"data must hold {need} bytes")
+        self.data = data
+        self.out_features = N
+        self.in_features = K
+        self.group = group
+        self.scale_dtype = scale_dtype
+
+    @property
+    def scale_type(self) -> int:
+        return _W4_SCALES[self.scale_dtype]
+
+
+def _w4_packed_bytes(N: int, K: int, group: int, scale_dtype: torch.dtype) -> int:
+    L = _lib.lib()
+    if int(L.bitlinear_w4_groups(K, group)) <= 0 or not 0 <= N < 1 << 31:
+        raise ValueError(f"invalid N = {N}, K = {K} or group = {group} (K % 16 == 0, group 32, 64 or 128)")
+    return int(L.bitlinear_w4_packed_bytes(N, K, group, _W4_SCALES[scale_dtype]))
+
+
+def pack_weights_w4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype = torch.float32,
+                    ws: Optional[torch.Tensor] = None) -> W4Weights:
+    """4-bit quantisation + pack: fp32 or bf16 W [N, K], one scale max|w|/7 per
+    `group` (32, 64 or 128) columns of a row. Synchronous; raises BitLinearError
+    (BL_ERR_NONFINITE) on Inf or NaN."""
+    sfx = _float_input(W, "W")
+    if W.dim() != 2:
+        raise ValueError("W must be [N, K]")
+    if scale_dtype not in _W4_SCALES:
+        raise TypeError(f"scales must be fp32 or bf16, got {scale_dtype}")
+    N, K = W.shape
+    data = torch.empty(_w4_packed_bytes(N, K, group, scale_dtype), dtype=torch.uint8, device=W.device)
+    if ws is None:
+        ws = _alloc_ws(_lib.lib().bitlinear_pack_workspace_size(N, K), W.device)
+    _same_device(ws, "ws", W.device)
+    with _on_device(W.device):
+        _lib.call("bitlinear_pack_weights_w4" + sfx, W.data_ptr(), N, K, group, _W4_SCALES[scale_dtype],
+                  data.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(W.device))
+    return W4Weights(data, N, K, group, scale_dtype)
+
+
+def import_w4(codes: torch.Tensor, S: torch.Tensor, group: int) -> W4Weights:
+    """Lay out a weight that is 4 bits already: codes uint8 [N, K/2] (column 2j
+    in the low nibble of byte j, stored as c + 8) and scales S [N, ceil(K/group)],
+    fp32 or bf16."""
+    _need_cuda(codes, "codes", torch.uint8)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [N, K/2]")
+    N, K = codes.shape[0], codes.shape[1] * 2
+    if S.dtype not in _W4_SCALES:
+        raise TypeError(f"S must be fp32 or bf16, got {S.dtype}")
+    _need_cuda(S, "S", S.dtype)
+    _same_device(S, "S", codes.device)
+    nbytes = _w4_packed_bytes(N, K, group, S.dtype)
+    if tuple(S.shape) != (N, -(-K // group)):
+        raise ValueError(f"S must have shape [{N}, {-(-K // group)}], got {list(S.shape)}")
+    data = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    with _on_device(codes.device):
+        _lib.call("bitlinear_w4_import", codes.data_ptr(), S.data_ptr(), N, K, group, _W4_SCALES[S.dtype],
+                  data.data_ptr(), _stream_handle(codes.device))
+    return W4Weights(data, N, K, group, S.dtype)
+
+
+def unpack_w4(w: W4Weights) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The codes (int8 [N, K], -8 .. 7) and scales [N, ceil(K/group)] of a packed weight."""
+    N, K = w.out_features, w.in_features
+    codes = torch.empty((N, K), dtype=torch.int8, device=w.data.device)
+    S = torch.empty((N, -(-K // w.group)), dtype=w.scale_dtype, device=w.data.device)
+    with _on_device(w.data.device):
+        _lib.call("bitlinear_w4_export", w.data.data_ptr(), N, K, w.group, w.scale_type, codes.data_ptr(),
+                  S.data_ptr(), _stream_handle(w.data.device))
+    return codes, S
+
+
+def w4_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.lib().bitlinear_w4_workspace_size(M, N, K))
+
+
+def w4_sample_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.lib().bitlinear_w4_sample_workspace_size(M, N, K))
+
+
+def _w4_input(x: torch.Tensor, w: W4Weights) -> str:
+    sfx = _float_input(x, "x")
+    if x.dim() != 2 or x.shape[1] != w.in_features:
+        raise ValueError(f"x must be [M, {w.in_features}], got {list(x.shape)}")
+    _same_device(x, "x", w.data.device)
+    return sfx
+
+
+def forward_w4(x: torch.Tensor, w: W4Weights, out: Optional[torch.Tensor] = None,
+               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] = x W^T from a 4-bit weight with group scales; x [M, K] fp32 or
+    bf16 (not quantised), y fp32. Calls that can overlap need a workspace each."""
+    sfx = _w4_input(x, w)
+    M, N, K = x.shape[0], w.out_features, w.in_features
+    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
+    _need_cuda(y, "out", torch.float32)
+    _same_device(y, "out", x.device)
+    if tuple(y.shape) != (M, N):
+        raise ValueError(f"out must have shape [{M}, {N}], got {list(y.shape)}")
+    if ws is None:
+        ws = _alloc_ws(w4_workspace_size(M, N, K), x.device)
+    _same_device(ws, "ws", x.device)
+    with _on_device(x.device):
+        _lib.call("bitlinear_forward_w4" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.data.data_ptr(),
+                  y.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(x.device))
+    return y
+
+
+def _sampling(B: int, device: torch.device, temperature, top_k, top_p, min_p) -> "_lib.Sampling":
+    how = _lib.Sampling()
+    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            _need_cuda(v, name, dtype)
+            _same_device(v, name, device)
+            if v.numel() != B:
+                raise ValueError(f"{name} must hold one value per row ({B}), got {v.numel()}")
+            setattr(how, name, v.data_ptr())
+        else:
+            setattr(how, name + "_value", v)
+    return how
+
+
+def _need_u(u: torch.Tensor, B: int, device: torch.device) -> None:
+    _need_cuda(u, "u", torch.float32)
+    _same_device(u, "u", device)
+    if u.numel() != B:
+        raise ValueError(f"u must hold one number per row ({B}), got {u.numel()}")
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0,
+           min_p=0.0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token per row of logits [B, V] (fp32 or bf16; rows may be apart) from
+    uniform numbers u [B] in [0, 1). Each setting is one number, or a tensor with one
+    per row (fp32; top_k int32): temperature (not > 0: the largest logit), then
+    top_k (<= 0: off), top_p (>= 1: off) of what top_k leaves, min_p (<= 0: off)
+    relative to the likeliest token. Returns (tokens int64 [B], log-probabilities
+    fp32 [B] under the filtered distribution); a row without a finite or +inf logit
+    gives (-1, -inf)."""
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be fp32 or bf16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [B, V] with neighbouring columns adjacent")
+    B, V = logits.shape
+    ld = logits.stride(0) if B > 1 else V
+    if ld < V:
+        raise ValueError("the rows of logits must not overlap")
+    _need_u(u, B, logits.device)
+    how = _sampling(B, logits.device, temperature, top_k, top_p, min_p)
+    tokens = torch.empty(B, dtype=torch.int64, device=logits.device)
+    logprobs = torch.empty(B, dtype=torch.float32, device=logits.device)
+    sfx = "_bf16" if logits.dtype == torch.bfloat16 else ""
+    with _on_device(logits.device):
+        _lib.call("bitlinear_sample" + sfx, logits.data_ptr(), B, V, ld, ctypes.byref(how), u.data_ptr(),
+                  tokens.data_ptr(), logprobs.data_ptr(), _stream_handle(logits.device))
+    return tokens, logprobs
+
+
+def forward_w4_sample(x: torch.Tensor, w: W4Weights, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                      ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The end of a decode step: sample(forward_w4(x, w), u, ...) in one call,
+    the logits staying in the workspace."""
+    sfx = _w4_input(x, w)
+    M, N, K = x.shape[0], w.out_features, w.in_features
+    _need_u(u, M, x.device)
+    how = _sampling(M, x.device, temperature, top_k, top_p, min_p)
+    tokens = torch.empty(M, dtype=torch.int64, device=x.device)
+    logprobs = torch.empty(M, dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = _alloc_ws(w4_sample_workspace_size(M, N, K), x.device)
+    _same_device(ws, "ws", x.device)
+    with _on_device(x.device):
+        _lib.call("bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type,
+                  w.data.data_ptr(), ctypes.byref(how), u.data_ptr(), tokens.data_ptr(), logprobs.data_ptr(),
+                  ws.data_ptr(), ws.numel(), _stream_handle(x.device))
+    return tokens, logprobs
 
 
 def forward_batch(calls, flags: int = 0, ws: Optional[torch.Tensor] = None):

@@ -1,6 +1,7 @@
 // bl_api.cu - the extern "C" entry points of libbitlinear (see include/bitlinear.h).
 // Host-side validation and dispatch only; all arithmetic of the path runs in
-// the kernels of bl_quant.cu, bl_decode.cu, bl_gemm.cu and bl_i2s.cu.
+// the kernels of bl_quant.cu, bl_decode.cu, bl_gemm.cu, bl_block.cu, bl_i2s.cu,
+// bl_w4.cu and bl_sample.cu.
 #include "bitlinear.h"
 #include "bl_internal.h"
 
@@ -420,6 +421,196 @@ int bitlinear_forward_blocks(const float* x, int64_t M, int64_t N, int64_t K, co
 int bitlinear_forward_blocks_bf16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
                                   const float* D, float* y, void* ws, size_t ws_bytes, bl_stream_t stream) {
   return forward_blocks_impl(x, true, M, N, K, packed, D, y, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------- 4-bit weights, sampling ------
+static int w4_shape(int64_t N, int64_t K, int group, int scale_type, bl::W4Shape* sh) {
+  const int st = check_k(K);
+  if (st != BL_OK) return st;
+  if (N < 0 || N > 0x7FFFFFFF) return BL_ERR_SHAPE;
+  if (group != 32 && group != 64 && group != 128) return BL_ERR_SHAPE;
+  if (scale_type != BL_SCALE_F32 && scale_type != BL_SCALE_BF16) return BL_ERR_SHAPE;
+  sh->N = N;
+  sh->K = K;
+  sh->group = group;
+  sh->scale_bytes = scale_type == BL_SCALE_F32 ? 4 : 2;
+  return BL_OK;
+}
+
+int64_t bitlinear_w4_groups(int64_t K, int group) {
+  bl::W4Shape sh;
+  return w4_shape(1, K, group, BL_SCALE_F32, &sh) == BL_OK ? sh.groups() : 0;
+}
+
+size_t bitlinear_w4_packed_bytes(int64_t N, int64_t K, int group, int scale_type) {
+  bl::W4Shape sh;
+  return w4_shape(N, K, group, scale_type, &sh) == BL_OK ? sh.bytes() : 0;
+}
+
+static int pack_w4_impl(const void* W, bool bf16, int64_t N, int64_t K, int group, int scale_type, void* packed,
+                        void* ws, size_t ws_bytes, bl_stream_t stream) {
+  bl::W4Shape sh;
+  const int st = w4_shape(N, K, group, scale_type, &sh);
+  if (st != BL_OK) return st;
+  if (N == 0) return BL_ERR_SHAPE;
+  if (W == nullptr || packed == nullptr || ws == nullptr) return BL_ERR_NULL;
+  if (!aligned16(W) || !aligned16(packed) || !aligned256(ws)) return BL_ERR_ALIGN;
+  if (ws_bytes < bl::kPackWsBytes) return BL_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return BL_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* word = static_cast<uint32_t*>(ws);
+  if (cudaMemsetAsync(word, 0, sizeof(uint32_t), s) != cudaSuccess) return BL_ERR_CUDA;
+  if (bl::launch_w4_pack(W, bf16, sh, packed, word, s, sms) != cudaSuccess) return BL_ERR_CUDA;
+  uint32_t status = 0;
+  if (cudaMemcpyAsync(&status, word, sizeof(status), cudaMemcpyDeviceToHost, s) != cudaSuccess) return BL_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return BL_ERR_CUDA;
+  return status == 0u ? BL_OK : BL_ERR_NONFINITE;
+}
+
+int bitlinear_pack_weights_w4(const float* W, int64_t N, int64_t K, int group, int scale_type, void* packed, void* ws,
+                              size_t ws_bytes, bl_stream_t stream) {
+  return pack_w4_impl(W, false, N, K, group, scale_type, packed, ws, ws_bytes, stream);
+}
+
+int bitlinear_pack_weights_w4_bf16(const uint16_t* W, int64_t N, int64_t K, int group, int scale_type, void* packed,
+                                   void* ws, size_t ws_bytes, bl_stream_t stream) {
+  return pack_w4_impl(W, true, N, K, group, scale_type, packed, ws, ws_bytes, stream);
+}
+
+int bitlinear_w4_import(const uint8_t* codes, const void* S, int64_t N, int64_t K, int group, int scale_type,
+                        void* packed, bl_stream_t stream) {
+  bl::W4Shape sh;
+  const int st = w4_shape(N, K, group, scale_type, &sh);
+  if (st != BL_OK) return st;
+  if (N == 0) return BL_OK;
+  if (codes == nullptr || S == nullptr || packed == nullptr) return BL_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(S) || !aligned16(packed)) return BL_ERR_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return BL_ERR_CUDA;
+  return cuda_status(bl::launch_w4_import(codes, S, sh, packed, reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+int bitlinear_w4_export(const void* packed, int64_t N, int64_t K, int group, int scale_type, int8_t* codes, void* S,
+                        bl_stream_t stream) {
+  bl::W4Shape sh;
+  const int st = w4_shape(N, K, group, scale_type, &sh);
+  if (st != BL_OK) return st;
+  if (N == 0) return BL_OK;
+  if (codes == nullptr || S == nullptr || packed == nullptr) return BL_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(S) || !aligned16(packed)) return BL_ERR_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return BL_ERR_CUDA;
+  return cuda_status(bl::launch_w4_export(packed, sh, codes, S, reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+size_t bitlinear_w4_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (check_k(K) != BL_OK || check_mn(M, N) != BL_OK) return 0;
+  return bl::ws_w4_bytes(M, K);
+}
+
+static int forward_w4_impl(const void* x, bool bf16, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                           const void* packed, float* y, void* ws, size_t ws_bytes, bl_stream_t stream) {
+  bl::W4Shape sh;
+  int st = w4_shape(N, K, group, scale_type, &sh);
+  if (st != BL_OK) return st;
+  st = check_mn(M, N);
+  if (st != BL_OK) return st;
+  if (M == 0 || N == 0) return BL_OK;
+  if (x == nullptr || packed == nullptr || y == nullptr || ws == nullptr) return BL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || !aligned256(ws)) return BL_ERR_ALIGN;
+  if (ws_bytes < bl::ws_w4_bytes(M, K)) return BL_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return BL_ERR_CUDA;
+  return cuda_status(
+      bl::launch_forward_w4(x, bf16, M, sh, packed, y, ws, reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+int bitlinear_forward_w4(const float* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                         const void* packed, float* y, void* ws, size_t ws_bytes, bl_stream_t stream) {
+  return forward_w4_impl(x, false, M, N, K, group, scale_type, packed, y, ws, ws_bytes, stream);
+}
+
+int bitlinear_forward_w4_bf16(const uint16_t* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                              const void* packed, float* y, void* ws, size_t ws_bytes, bl_stream_t stream) {
+  return forward_w4_impl(x, true, M, N, K, group, scale_type, packed, y, ws, ws_bytes, stream);
+}
+
+// Checks of the sampler's arguments besides the logits.
+static int check_sample(int64_t B, int64_t V, const bl_sampling* how, const float* u, const int64_t* tokens,
+                        const float* logprobs) {
+  if (B < 0 || B > 0x7FFFFFFF || V < 1 || V > bl::kSampleMaxV) return BL_ERR_SHAPE;
+  if (B == 0) return BL_OK;
+  if (how == nullptr || u == nullptr || tokens == nullptr) return BL_ERR_NULL;
+  const auto off = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; };
+  if (off(how->temperature, 4) || off(how->top_k, 4) || off(how->top_p, 4) || off(how->min_p, 4) || off(u, 4) ||
+      off(tokens, 8) || off(logprobs, 4))
+    return BL_ERR_ALIGN;
+  return BL_OK;
+}
+
+static bl::SampleHow sample_how(const bl_sampling* h) {
+  return bl::SampleHow{h->temperature,       h->top_k,       h->top_p,       h->min_p,
+                       h->temperature_value, h->top_k_value, h->top_p_value, h->min_p_value};
+}
+
+static int sample_impl(const void* logits, bool bf16, int64_t B, int64_t V, int64_t ld, const bl_sampling* how,
+                       const float* u, int64_t* tokens, float* logprobs, bl_stream_t stream) {
+  const int st = check_sample(B, V, how, u, tokens, logprobs);
+  if (st != BL_OK) return st;
+  if (ld < V) return BL_ERR_SHAPE;
+  if (B == 0) return BL_OK;
+  if (logits == nullptr) return BL_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) != 0) return BL_ERR_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return BL_ERR_CUDA;
+  return cuda_status(bl::launch_sample(logits, bf16, B, V, ld, sample_how(how), u, tokens, logprobs,
+                                       reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+int bitlinear_sample(const float* logits, int64_t B, int64_t V, int64_t ld, const bl_sampling* how, const float* u,
+                     int64_t* tokens, float* logprobs, bl_stream_t stream) {
+  return sample_impl(logits, false, B, V, ld, how, u, tokens, logprobs, stream);
+}
+
+int bitlinear_sample_bf16(const uint16_t* logits, int64_t B, int64_t V, int64_t ld, const bl_sampling* how,
+                          const float* u, int64_t* tokens, float* logprobs, bl_stream_t stream) {
+  return sample_impl(logits, true, B, V, ld, how, u, tokens, logprobs, stream);
+}
+
+size_t bitlinear_w4_sample_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (check_k(K) != BL_OK || check_mn(M, N) != BL_OK) return 0;
+  return bl::ws_w4_bytes(M, K) + bl::align256(4 * (size_t)M * (size_t)N);
+}
+
+static int w4_sample_impl(const void* x, bool bf16, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                          const void* packed, const bl_sampling* how, const float* u, int64_t* tokens,
+                          float* logprobs, void* ws, size_t ws_bytes, bl_stream_t stream) {
+  int st = check_mn(M, N);
+  if (st != BL_OK) return st;
+  st = check_sample(M, N, how, u, tokens, logprobs);
+  if (st != BL_OK) return st;
+  if (check_k(K) != BL_OK) return BL_ERR_SHAPE;
+  if (M == 0) return BL_OK;
+  if (ws == nullptr) return BL_ERR_NULL;
+  if (ws_bytes < bitlinear_w4_sample_workspace_size(M, N, K)) return BL_ERR_WORKSPACE;
+  const size_t fwd = bl::ws_w4_bytes(M, K);
+  float* logits = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + fwd);
+  st = forward_w4_impl(x, bf16, M, N, K, group, scale_type, packed, logits, ws, fwd, stream);
+  if (st != BL_OK) return st;
+  return sample_impl(logits, false, M, N, N, how, u, tokens, logprobs, stream);
+}
+
+int bitlinear_forward_w4_sample(const float* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                                const void* packed, const bl_sampling* how, const float* u, int64_t* tokens,
+                                float* logprobs, void* ws, size_t ws_bytes, bl_stream_t stream) {
+  return w4_sample_impl(x, false, M, N, K, group, scale_type, packed, how, u, tokens, logprobs, ws, ws_bytes, stream);
+}
+
+int bitlinear_forward_w4_sample_bf16(const uint16_t* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                                     const void* packed, const bl_sampling* how, const float* u, int64_t* tokens,
+                                     float* logprobs, void* ws, size_t ws_bytes, bl_stream_t stream) {
+  return w4_sample_impl(x, true, M, N, K, group, scale_type, packed, how, u, tokens, logprobs, ws, ws_bytes, stream);
 }
 
 size_t bitlinear_batch_workspace_size(const bl_linear_call* calls, int count) {

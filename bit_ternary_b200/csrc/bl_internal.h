@@ -135,6 +135,56 @@ inline size_t ws_blocks_bytes(int64_t M, int64_t K) {
 cudaError_t launch_forward_blocks(const void* x, bool bf16, int64_t M, int64_t N, int64_t K, const uint32_t* packed,
                                   const float* D, float* y, void* ws, cudaStream_t stream, int num_sms);
 
+// 4-bit weights with group scales (bl_w4.cu). The packed buffer is a run of
+// 16-row tiles, each a run of ceil(K / 128) blocks. A block is 16 rows x 64
+// bytes of codes, then its 128 / group scales of each row, [group][row]. Row r
+// of a block holds 16 words, word 4*t + j the columns 32*j + 8*t .. + 7: the
+// 16 bytes that lane (r % 8, t) of a 16x8x16 matrix instruction takes from the
+// row, so a warp's load of eight rows is 512 consecutive bytes, and a thread
+// that owns a whole row reads 64. Nibble p of a word (p < 4) is column 2p of
+// its eight, nibble 4 + p column 2p + 1: (word >> 4p) & 0x000F000F is a pair
+// of neighbouring columns in the halves of a register. Stored as c + 8.
+constexpr int kW4Rows = 16;
+constexpr int kW4Cols = 128;
+constexpr int kW4CodeBytes = kW4Rows * kW4Cols / 2;
+struct W4Shape {
+  int64_t N, K;
+  int group;       // 32, 64 or 128
+  int scale_bytes; // 4 (fp32) or 2 (bf16)
+  __host__ __device__ int64_t tiles() const { return (N + kW4Rows - 1) / kW4Rows; }
+  __host__ __device__ int64_t blocks() const { return (K + kW4Cols - 1) / kW4Cols; }
+  __host__ __device__ int64_t groups() const { return (K + group - 1) / group; }
+  __host__ __device__ int block_bytes() const { return kW4CodeBytes + kW4Rows * (kW4Cols / group) * scale_bytes; }
+  __host__ __device__ size_t bytes() const { return (size_t)tiles() * (size_t)blocks() * (size_t)block_bytes(); }
+};
+// status: a device word that gets bit 0 OR-ed in for a group holding a
+// non-finite weight (that group is packed as zeros).
+cudaError_t launch_w4_pack(const void* W, bool bf16, const W4Shape& sh, void* packed, uint32_t* status,
+                           cudaStream_t stream, int num_sms);
+cudaError_t launch_w4_import(const uint8_t* codes, const void* S, const W4Shape& sh, void* packed,
+                             cudaStream_t stream, int num_sms);
+cudaError_t launch_w4_export(const void* packed, const W4Shape& sh, int8_t* codes, void* S, cudaStream_t stream,
+                             int num_sms);
+inline size_t ws_w4_bytes(int64_t M, int64_t K) { return kHeaderBytes + align256(6 * (size_t)M * (size_t)K); }
+// x is fp32, or bf16 bit patterns when bf16.
+cudaError_t launch_forward_w4(const void* x, bool bf16, int64_t M, const W4Shape& sh, const void* packed, float* y,
+                              void* ws, cudaStream_t stream, int num_sms);
+
+// Sampling (bl_sample.cu). Settings as in bl_sampling.
+constexpr int64_t kSampleMaxV = 4194304;
+struct SampleHow {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_value;
+  int32_t top_k_value;
+  float top_p_value;
+  float min_p_value;
+};
+cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, int64_t ld, const SampleHow& how,
+                          const float* u, int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms);
+
 cudaError_t launch_selftest_wait(uint32_t* err, uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace bl

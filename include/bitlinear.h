@@ -295,6 +295,126 @@ BL_API int bitlinear_forward_blocks_bf16(const uint16_t* x, int64_t M, int64_t N
                                          const uint32_t* packed, const float* D, float* y,
                                          void* ws, size_t ws_bytes, bl_stream_t stream);
 
+/* ------------------------------------- 4-bit weights with group scales --- */
+
+/* The sibling of the per-block variant for layers that are kept at 4 bits (a
+ * model's output matrix above all):
+ *   W[n,k] = S[n, k/group] * c[n,k],   c in -8 .. 7, group in {32, 64, 128}
+ *   y[m,n] = sum_G S[n,G] * ( sum over k in G of c[n,k] * x[m,k] )
+ * K % 16 == 0; a row has G = ceil(K / group) scales, the last group may be
+ * short. x is fp32 or bf16 and is not quantised; S is fp32 or bf16; y is fp32.
+ * The codes and their products with x are exact (an fp32 x takes part as its
+ * three 8-bit significand pieces), the sums are held in fp32, and the scale is
+ * applied to a group's sum. A non-finite x[m,k] reaches y[m,:] only.
+ *
+ * `packed` is one opaque buffer of bitlinear_w4_packed_bytes() bytes (16-byte
+ * aligned), laid out once per weight: 16-row tiles, each a run of 128-column
+ * blocks, each block 16 rows x 64 bytes of codes followed by the block's
+ * scales. Rows past N and columns past K hold the code 0. */
+#define BL_SCALE_F32 0
+#define BL_SCALE_BF16 1
+
+/* G = ceil(K / group); 0 for an invalid K or group. */
+BL_API int64_t bitlinear_w4_groups(int64_t K, int group);
+
+/* Bytes of the packed buffer; 0 for invalid sizes. */
+BL_API size_t bitlinear_w4_packed_bytes(int64_t N, int64_t K, int group, int scale_type);
+
+/* Quantise and pack: per group a = max|w|, S = RN(a / 7) (rounded once more
+ * to bf16 for BL_SCALE_BF16), c = clamp(rint(RN(w / S)), -8, 7); S = 0 and
+ * c = 0 where S rounds to zero.
+ *   W       device fp32 [N, K], read only.
+ *   packed  device buffer, fully overwritten.
+ *   ws      device scratch of ws_bytes >= bitlinear_pack_workspace_size().
+ * Synchronous (it reads back the status word). BL_ERR_NONFINITE if a group
+ * holds Inf or NaN; that group is packed as zeros. N >= 1 is required. */
+BL_API int bitlinear_pack_weights_w4(const float* W, int64_t N, int64_t K, int group, int scale_type, void* packed,
+                                     void* ws, size_t ws_bytes, bl_stream_t stream);
+
+/* As bitlinear_pack_weights_w4, from a bf16 weight (bit patterns [N, K],
+ * uint16, 16-byte aligned), each value widened to fp32 exactly. Synchronous. */
+BL_API int bitlinear_pack_weights_w4_bf16(const uint16_t* W, int64_t N, int64_t K, int group, int scale_type,
+                                          void* packed, void* ws, size_t ws_bytes, bl_stream_t stream);
+
+/* Lay out codes that are 4 bits already: codes device uint8 [N, K/2], two to
+ * a byte (column 2j in the low nibble of byte j), stored as c + 8; S device
+ * [N, G] of scale_type. Asynchronous. */
+BL_API int bitlinear_w4_import(const uint8_t* codes, const void* S, int64_t N, int64_t K, int group, int scale_type,
+                               void* packed, bl_stream_t stream);
+
+/* The inverse: codes device int8 [N, K] (the values c, one to a byte) and S
+ * [N, G] of scale_type. Asynchronous. */
+BL_API int bitlinear_w4_export(const void* packed, int64_t N, int64_t K, int group, int scale_type, int8_t* codes,
+                               void* S, bl_stream_t stream);
+
+/* Bytes of scratch that bitlinear_forward_w4 needs (x of either type). */
+BL_API size_t bitlinear_w4_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* y [M, N] fp32 from x [M, K] fp32 and a packed 4-bit weight. All pointers
+ * 16-byte aligned, ws 256-byte aligned. Calls that can overlap need a
+ * workspace each. bitlinear_workspace_error() reads ws. Asynchronous. */
+BL_API int bitlinear_forward_w4(const float* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                                const void* packed, float* y, void* ws, size_t ws_bytes, bl_stream_t stream);
+
+/* As bitlinear_forward_w4, from bf16 x (bit patterns [M, K], uint16). */
+BL_API int bitlinear_forward_w4_bf16(const uint16_t* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                                     const void* packed, float* y, void* ws, size_t ws_bytes, bl_stream_t stream);
+
+/* ------------------------------------------------------------- sampling --- */
+
+/* How the token of a row of logits is chosen. Each setting is a device array
+ * [B] or, where its pointer is NULL, one value for every row. */
+typedef struct {
+  const float* temperature;  /* T; not > 0: the row's largest logit is taken */
+  const int32_t* top_k;      /* k <= 0: off */
+  const float* top_p;        /* p >= 1 or NaN: off */
+  const float* min_p;        /* m <= 0 or NaN: off; m > 1 counts as 1 */
+  float temperature_value;
+  int32_t top_k_value;
+  float top_p_value;
+  float min_p_value;
+} bl_sampling;
+
+/* One token per row of logits [B, V] (device fp32, rows ld elements apart,
+ * ld >= V, element-aligned) from given uniform numbers u [B] in [0, 1):
+ *   Tokens whose logit is NaN or -inf are out. m = the largest logit,
+ *   w_i = exp((x_i - m) / T). With m = +inf the tokens at +inf have w = 1, all
+ *   others 0.
+ *   top-k keeps the first k tokens in the order (x descending, index
+ *   ascending); top-p the shortest prefix of these, at least one token, whose
+ *   sum of w reaches p times their sum; min-p those of these with w >= m.
+ *   The token is the first kept index, in ascending order, whose running sum
+ *   of w exceeds u times the kept sum (u NaN or < 0 counts as 0, u >= 1 takes
+ *   the last token of positive weight).
+ * The sums run over w rounded to multiples of 2^-40, exactly, so the token does not
+ * depend on any order of adding.
+ *   tokens    device int64 [B]: the index, or -1 where every token is out.
+ *   logprobs  device fp32 [B] or NULL: ln(w / kept sum) of the token (0 for
+ *             T not > 0, -inf for -1).
+ * 0 <= B < 2^31, 1 <= V <= 4194304. B == 0 is a no-op. Asynchronous. */
+BL_API int bitlinear_sample(const float* logits, int64_t B, int64_t V, int64_t ld, const bl_sampling* how,
+                            const float* u, int64_t* tokens, float* logprobs, bl_stream_t stream);
+
+/* As bitlinear_sample, from bf16 logits (bit patterns, uint16). */
+BL_API int bitlinear_sample_bf16(const uint16_t* logits, int64_t B, int64_t V, int64_t ld, const bl_sampling* how,
+                                 const float* u, int64_t* tokens, float* logprobs, bl_stream_t stream);
+
+/* Bytes of scratch for bitlinear_forward_w4_sample: the forward's workspace
+ * and the logits. */
+BL_API size_t bitlinear_w4_sample_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* The end of a decode step: logits = bitlinear_forward_w4(x) over a packed
+ * output matrix, then bitlinear_sample of every row (u, tokens, logprobs [M]).
+ * The logits stay in ws. x fp32, or bf16 bit patterns for _bf16. N <= 4194304.
+ * Asynchronous. */
+BL_API int bitlinear_forward_w4_sample(const float* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
+                                       const void* packed, const bl_sampling* how, const float* u, int64_t* tokens,
+                                       float* logprobs, void* ws, size_t ws_bytes, bl_stream_t stream);
+BL_API int bitlinear_forward_w4_sample_bf16(const uint16_t* x, int64_t M, int64_t N, int64_t K, int group,
+                                            int scale_type, const void* packed, const bl_sampling* how,
+                                            const float* u, int64_t* tokens, float* logprobs, void* ws,
+                                            size_t ws_bytes, bl_stream_t stream);
+
 /* ---------------------------------------------------------------- batch --- */
 
 /* One BitLinear of a batch: y [M,N] = F.linear(ActQuant(x [M,K]), W) from
