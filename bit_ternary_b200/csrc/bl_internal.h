@@ -137,7 +137,8 @@ cudaError_t launch_forward_blocks(const void* x, bool bf16, int64_t M, int64_t N
 
 // 4-bit weights with group scales (bl_w4.cu). The packed buffer is a run of
 // 16-row tiles, each a run of ceil(K / 128) blocks. A block is 16 rows x 64
-// bytes of codes, then its 128 / group scales of each row, [group][row]. Row r
+// bytes of codes, then its 128 / group scales of each row, [row % 8][group]
+// [row / 8] (a lane's two rows and all their groups side by side). Row r
 // of a block holds 16 words, word 4*t + j the columns 32*j + 8*t .. + 7: the
 // 16 bytes that lane (r % 8, t) of a 16x8x16 matrix instruction takes from the
 // row, so a warp's load of eight rows is 512 consecutive bytes, and a thread
@@ -153,6 +154,9 @@ struct W4Shape {
   int scale_bytes; // 4 (fp32) or 2 (bf16)
   __host__ __device__ int64_t tiles() const { return (N + kW4Rows - 1) / kW4Rows; }
   __host__ __device__ int64_t blocks() const { return (K + kW4Cols - 1) / kW4Cols; }
+  __host__ __device__ int scale_index(int row, int gi) const {  // row of 16, group of the block
+    return ((row & 7) * (kW4Cols / group) + gi) * 2 + (row >> 3);
+  }
   __host__ __device__ int64_t groups() const { return (K + group - 1) / group; }
   __host__ __device__ int block_bytes() const { return kW4CodeBytes + kW4Rows * (kW4Cols / group) * scale_bytes; }
   __host__ __device__ size_t bytes() const { return (size_t)tiles() * (size_t)blocks() * (size_t)block_bytes(); }
@@ -165,6 +169,43 @@ cudaError_t launch_w4_import(const uint8_t* codes, const void* S, const W4Shape&
                              cudaStream_t stream, int num_sms);
 cudaError_t launch_w4_export(const void* packed, const W4Shape& sh, int8_t* codes, void* S, cudaStream_t stream,
                              int num_sms);
+// The three bf16 pieces of an fp32 x: its significand cut into 8 + 8 + 8 bits,
+// so h + m + l == x exactly (bits under 2^-133, which only |x| < 2^-110 can
+// have, are dropped). A non-finite x is h alone.
+__device__ __forceinline__ void split_bf16x3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
+  const uint32_t b = __float_as_uint(x);
+  if ((b & 0x7F800000u) == 0x7F800000u) {
+    h = (b >> 16) | ((b & 0x007FFFFFu) != 0u ? 0x0040u : 0u);  // a NaN stays one
+    m = 0u;
+    l = 0u;
+    return;
+  }
+  h = b >> 16;
+  const float r = x - __uint_as_float(b & 0xFFFF0000u);
+  const uint32_t rb = __float_as_uint(r);
+  m = rb >> 16;
+  l = __float_as_uint(r - __uint_as_float(rb & 0xFFFF0000u)) >> 16;
+}
+// Eight codes of a packed word to four bf16 pairs of c * 2^-6. A bf16 whose
+// bits are an integer v below 256 is v * 2^-133 (subnormals and the first
+// binade are one line), so a nibble masked out where it stands, at bit 0 or at
+// bit 4 of a half, is u * 2^-133 or u * 2^-129 without a shift or an offset.
+// One fused multiply-add, exact, brings both to (u - 8) * 2^-6 = c * 2^-6:
+// nine instructions a word, five of them on the integer pipe.
+constexpr float kW4Unit = 64.0f;  // 2^6, what a sum of products is multiplied by
+__device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&pair)[4]) {
+  const uint32_t v = w >> 8;
+  const uint32_t off = 0xBE00BE00u;                          // -8 * 2^-6
+  const uint32_t up0 = 0x7F007F00u, up1 = 0x7D007D00u;       // 2^127, 2^123
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(pair[0]) : "r"(w & 0x000F000Fu), "r"(up0), "r"(off));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(pair[1]) : "r"(w & 0x00F000F0u), "r"(up1), "r"(off));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(pair[2]) : "r"(v & 0x000F000Fu), "r"(up0), "r"(off));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(pair[3]) : "r"(v & 0x00F000F0u), "r"(up1), "r"(off));
+}
+// The one-launch kernel for few tokens (bl_w4.cu) holds x in shared memory as
+// bf16 columns: a token of bf16 x is one, a token of fp32 x three.
+constexpr int kW4StreamCols = 16;
+bool w4_stream_fits(int64_t M, bool bf16, const W4Shape& sh);
 inline size_t ws_w4_bytes(int64_t M, int64_t K) { return kHeaderBytes + align256(6 * (size_t)M * (size_t)K); }
 // x is fp32, or bf16 bit patterns when bf16.
 cudaError_t launch_forward_w4(const void* x, bool bf16, int64_t M, const W4Shape& sh, const void* packed, float* y,

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const void* __restrict__ W
     if ((lane & 1) == 0) reinterpret_cast<uint32_t*>(blk)[r * 16 + 4 * (wi & 3) + (wi >> 2)] = word;
     if ((lane % glanes) == 0) {
       uint8_t* sp = blk + kW4CodeBytes;
-      const int si = (lane / glanes) * kW4Rows + r;
+      const int si = sh.scale_index(r, lane / glanes);
       if (sh.scale_bytes == 4)
         reinterpret_cast<float*>(sp)[si] = s;
       else
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) w4_import_kernel(const uint8_t* __restric
     uint8_t* blk = packed + w4_block_off(sh, n / kW4Rows, kb);
     reinterpret_cast<uint32_t*>(blk)[r * 16 + 4 * (w & 3) + (w >> 2)] = word;
     if ((8 * w) % sh.group == 0) {
-      const int si = (8 * w / sh.group) * kW4Rows + r;
+      const int si = sh.scale_index(r, 8 * w / sh.group);
       const int64_t src = n * sh.groups() + k / sh.group;
       uint8_t* sp = blk + kW4CodeBytes;
       if (sh.scale_bytes == 4)
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) w4_export_kernel(const uint8_t* __restric
     }
     *reinterpret_cast<uint2*>(codes + n * sh.K + wi * 8) = make_uint2(out[0], out[1]);
     if ((8 * w) % sh.group == 0) {
-      const int si = (8 * w / sh.group) * kW4Rows + r;
+      const int si = sh.scale_index(r, 8 * w / sh.group);
       const int64_t dst = n * sh.groups() + wi * 8 / sh.group;
       const uint8_t* sp = blk + kW4CodeBytes;
       if (sh.scale_bytes == 4)
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(256) w4_plain_kernel(const void* __restrict__ 
       const int w = (int)(wi & 15);
       const uint8_t* blk = packed + w4_block_off(sh, n / kW4Rows, wi >> 4);
       const uint32_t word = reinterpret_cast<const uint32_t*>(blk)[r * 16 + 4 * (w & 3) + (w >> 2)];
-      const float s = w4_scale_load(blk + kW4CodeBytes, (8 * w / sh.group) * kW4Rows + r, sh.scale_bytes);
+      const float s = w4_scale_load(blk + kW4CodeBytes, sh.scale_index(r, 8 * w / sh.group), sh.scale_bytes);
       float c[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = (float)((int)((word >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - 8);
@@ -196,6 +196,349 @@ __global__ void __launch_bounds__(256) w4_plain_kernel(const void* __restrict__ 
       if (lane == 0 && m0 + i < M) y[(m0 + i) * sh.N + n] = v;
     }
   }
+}
+
+// ------------------------------------------------- few tokens: one stream --
+// The weights are the traffic: 1 KiB of codes and 32..256 bytes of scales per
+// block of 16 rows x 128 columns, read once. A CTA owns a run of whole row
+// tiles, and its warps equal runs of that run's blocks, wherever tiles begin or
+// end in it (an even split of whole tiles left a fifth of the machine idle). A
+// warp keeps kDepth blocks in registers, loaded 512 consecutive bytes at a
+// time and refilled as soon as they have been used. Codes become bf16
+// pairs (w4_unpack) and are multiplied with mma.sync m16n8k16: the weights are
+// the 16-row operand, up to 8 columns of x the other. bf16 codes and their
+// products are exact; a group's sum stays in fp32 and is multiplied by its
+// scale once. A tile that several warps share is added up through shared
+// memory in warp order after one barrier at the end. At full stream rate an SM has 47 cycles a
+// block, and its integer pipe takes 2 cycles per warp instruction: what is not
+// unpacking is kept off it (columns past the last token read a row of zeros
+// instead of being masked, products start from a zero register).
+constexpr int kStreamWarps = 8;
+constexpr int kStreamPadBytes = 64;  // column stride = 64 mod 128: no bank conflicts between columns
+constexpr size_t kStreamSmemMax = 225 * 1024;
+
+struct StreamParams {
+  const void* x;
+  const uint8_t* packed;
+  float* y;
+  uint32_t* err;
+  int M, K;
+  int64_t N;
+  int cols;     // columns of x: M, or 3 M for fp32
+  int blocks;   // 128-column blocks per row
+  int64_t tiles;
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 ldg_stream128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg_stream64(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg_stream32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+// d = a * b (+ d)
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One block of a lane: its 16 code bytes of rows g and g + 8, and the scales of
+// both rows for the block's groups.
+template <int GPB, bool kBf16S>
+struct LaneBlock {
+  static constexpr int kScaleWords = kBf16S ? GPB : 2 * GPB;
+  uint4 w0, w1;
+  uint32_t s[kScaleWords];
+  // src: the block's first byte plus 16 * lane; scales: the lane's scales.
+  __device__ __forceinline__ void load(const uint8_t* src, const uint8_t* scales) {
+    w0 = ldg_stream128(src);
+    w1 = ldg_stream128(src + 512);
+    if (kScaleWords == 1) {
+      s[0] = ldg_stream32(scales);
+    } else if (kScaleWords == 2) {
+      const uint2 v = ldg_stream64(scales);
+      s[0] = v.x;
+      s[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScaleWords; i += 4) {
+        const uint4 v = ldg_stream128(scales + 4 * i);
+        s[i] = v.x;
+        s[i + 1] = v.y;
+        s[i + 2] = v.z;
+        s[i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float scale(int gi, int half) const {
+    if (kBf16S) return __uint_as_float(half == 0 ? s[gi] << 16 : s[gi] & 0xFFFF0000u);
+    return __uint_as_float(s[2 * gi + half]);
+  }
+};
+
+// tot += scales * (codes * x) over one block; xb[nt] + xk: the lane's x.
+template <int NT, int GPB, bool kBf16S>
+__device__ __forceinline__ void stream_block(const LaneBlock<GPB, kBf16S>& blk, const uint32_t (&xb)[NT], uint32_t xk,
+                                             float (&tot)[NT][4]) {
+  const uint32_t w0[4] = {blk.w0.x, blk.w0.y, blk.w0.z, blk.w0.w};
+  const uint32_t w1[4] = {blk.w1.x, blk.w1.y, blk.w1.z, blk.w1.w};
+#pragma unroll
+  for (int gi = 0; gi < GPB; ++gi) {
+    float acc[NT][4];
+#pragma unroll
+    for (int jj = 0; jj < 4 / GPB; ++jj) {
+      const int j = gi * (4 / GPB) + jj;
+      uint32_t a[4], b[4];
+      w4_unpack(w0[j], a);
+      w4_unpack(w1[j], b);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 xv = lds128(xb[nt] + xk + 64 * j);
+        if (jj == 0)
+          mma_bf16_first(acc[nt], a[0], b[0], a[1], b[1], xv.x, xv.y);
+        else
+          mma_bf16(acc[nt], a[0], b[0], a[1], b[1], xv.x, xv.y);
+        mma_bf16(acc[nt], a[2], b[2], a[3], b[3], xv.z, xv.w);
+      }
+    }
+    const float s0 = blk.scale(gi, 0), s1 = blk.scale(gi, 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      tot[nt][0] = fmaf(s0, acc[nt][0], tot[nt][0]);
+      tot[nt][1] = fmaf(s0, acc[nt][1], tot[nt][1]);
+      tot[nt][2] = fmaf(s1, acc[nt][2], tot[nt][2]);
+      tot[nt][3] = fmaf(s1, acc[nt][3], tot[nt][3]);
+    }
+  }
+}
+
+// CTAs per SM: as many as the registers of a kDepth-block ring allow.
+template <int NT>
+constexpr int stream_ctas() { return NT == 1 ? 3 : 2; }
+
+template <int NT, bool kBf16X, int GPB, bool kBf16S>
+__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_stream_kernel(const StreamParams p) {
+  constexpr int kScaleBytes = kW4Rows * GPB * (kBf16S ? 2 : 4);
+  constexpr int kBlockBytes = kW4CodeBytes + kScaleBytes;
+  constexpr int kCols = 8 * NT;
+  constexpr int kDepth = kScaleBytes > 64 ? 2 : 3;
+  constexpr int kPart = kW4Rows * kCols;  // one warp's sums of a tile
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int xstride = p.blocks * kW4Cols * 2 + kStreamPadBytes;
+  // [warp][slot][row][col]: slot 0 a tile that an earlier warp began, 1 a tile
+  // that a later warp ends, 2 a whole tile.
+  float* part = reinterpret_cast<float*>(smem);
+  uint8_t* xs = smem + 3 * kStreamWarps * kPart * 4;
+
+  const int64_t tile0 = p.tiles * blockIdx.x / gridDim.x, tile1 = p.tiles * (blockIdx.x + 1) / gridDim.x;
+  const int64_t run = (tile1 - tile0) * p.blocks;
+  const auto warp_begin = [&](int w) { return run * w / kStreamWarps; };
+  const int64_t b0 = warp_begin(warp), b1 = warp_begin(warp + 1);
+  const uint8_t* src = p.packed + (tile0 * p.blocks + b0) * kBlockBytes + 16 * lane;
+  const int soff = kW4CodeBytes - 16 * lane + g * (kScaleBytes / 8);
+  int64_t left = b1 - b0;
+  LaneBlock<GPB, kBf16S> ring[kDepth];
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i)
+    if (i < left) ring[i].load(src + i * kBlockBytes, src + i * kBlockBytes + soff);
+
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0u;
+  // x to bf16 columns (column piece * M + m), zeros past K; then one column of zeros.
+  const int kpad = p.blocks * kW4Cols;
+  if (kBf16X) {
+    const int per = kpad / 8;
+    for (int i = threadIdx.x; i < p.M * per; i += kStreamWarps * 32) {
+      const int m = i / per, k = (i - m * per) * 8;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (k < p.K)
+        v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + (int64_t)m * p.K + k);
+      *reinterpret_cast<uint4*>(xs + (size_t)m * xstride + k * 2) = v;
+    }
+  } else {
+    const int per = kpad / 4;
+    for (int i = threadIdx.x; i < p.M * per; i += kStreamWarps * 32) {
+      const int m = i / per, k = (i - m * per) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < p.K) v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + (int64_t)m * p.K + k);
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      uint32_t h[4], mi[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_bf16x3(f[j], h[j], mi[j], l[j]);
+      uint8_t* d = xs + (size_t)m * xstride + k * 2;
+      const size_t plane = (size_t)p.M * xstride;
+      *reinterpret_cast<uint2*>(d) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      *reinterpret_cast<uint2*>(d + plane) = make_uint2(mi[0] | (mi[1] << 16), mi[2] | (mi[3] << 16));
+      *reinterpret_cast<uint2*>(d + 2 * plane) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+    }
+  }
+  for (int i = threadIdx.x; i < kpad / 8; i += kStreamWarps * 32)
+    *reinterpret_cast<uint4*>(xs + (size_t)p.cols * xstride + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+
+  uint32_t xb[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+    xb[nt] = smem_u32(xs) + (8 * nt + g < p.cols ? 8 * nt + g : p.cols) * xstride + 16 * t;
+  float tot[NT][4];
+  const auto clear = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tot[nt][i] = 0.f;
+  };
+  const auto store_part = [&](int slot) {
+    float* mine = part + (warp * 3 + slot) * kPart;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      *reinterpret_cast<float2*>(mine + g * kCols + 8 * nt + 2 * t) = make_float2(tot[nt][0], tot[nt][1]);
+      *reinterpret_cast<float2*>(mine + (g + 8) * kCols + 8 * nt + 2 * t) = make_float2(tot[nt][2], tot[nt][3]);
+    }
+  };
+  // y of a tile: this warp's sums in `slot`, and where `end` is not 0 slot 0 of
+  // the warps after it whose run begins before block `end` of the CTA's run
+  // (an empty run, of a CTA with fewer blocks than warps, holds nothing). Row
+  // fastest, so 16 neighbouring y are written together.
+  const auto write_tile = [&](int64_t tile, int slot, int64_t end) {
+    const float* from = part + (warp * 3 + slot) * kPart;
+    for (int i = lane; i < kW4Rows * p.M; i += 32) {
+      const int row = i & (kW4Rows - 1), m = i / kW4Rows;
+      const int64_t n = tile * kW4Rows + row;
+      const int at = row * kCols + m;
+      float v = from[at], mi = 0.f, l = 0.f;
+      if (!kBf16X) {
+        mi = from[at + p.M];
+        l = from[at + 2 * p.M];
+      }
+      for (int w = warp + 1; w < kStreamWarps && warp_begin(w) < end; ++w) {
+        if (warp_begin(w) == warp_begin(w + 1)) continue;
+        const float* q = part + w * 3 * kPart + at;
+        v += q[0];
+        if (!kBf16X) {
+          mi += q[p.M];
+          l += q[2 * p.M];
+        }
+      }
+      if (n < p.N) p.y[(int64_t)m * p.N + n] = (v + (mi + l)) * kW4Unit;
+    }
+  };
+  clear();
+  int64_t tile = tile0 + b0 / p.blocks;
+  int kb = (int)(b0 % p.blocks);  // block of the tile
+  bool head = kb != 0;            // the tile was begun by an earlier warp
+  const uint32_t xend = p.blocks * (kW4Cols * 2);
+  uint32_t xk = kb * (kW4Cols * 2);
+  while (left > 0) {
+    src += kDepth * kBlockBytes;
+    const uint8_t* ssrc = src + soff;
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) {
+      if (i < left) {
+        stream_block<NT, GPB, kBf16S>(ring[i], xb, xk, tot);
+        xk += kW4Cols * 2;
+        if (xk == xend) {
+          store_part(head ? 0 : 2);
+          if (!head) {
+            __syncwarp();
+            write_tile(tile, 2, 0);
+            __syncwarp();
+          }
+          clear();
+          head = false;
+          xk = 0;
+          ++tile;
+        }
+      }
+      if (i + kDepth < left) ring[i].load(src + i * kBlockBytes, ssrc + i * kBlockBytes);
+    }
+    left -= kDepth;
+  }
+  if (xk != 0 && b1 > b0) store_part(head ? 0 : 1);
+  __syncthreads();
+  // The warp in which a shared tile begins adds it up.
+  if (xk != 0 && b1 > b0 && !head) write_tile(tile, 1, (tile + 1 - tile0) * p.blocks);
+}
+
+size_t w4_stream_smem(int NT, int64_t cols, const W4Shape& sh) {
+  return (size_t)3 * kStreamWarps * kW4Rows * (8 * NT) * 4 +
+         (size_t)(cols + 1) * ((size_t)sh.blocks() * kW4Cols * 2 + kStreamPadBytes);
+}
+
+template <int NT, bool kBf16X, int GPB, bool kBf16S>
+cudaError_t launch_w4_stream_t(const StreamParams& p, int grid, size_t smem, cudaStream_t stream) {
+  auto kern = w4_stream_kernel<NT, kBf16X, GPB, kBf16S>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kStreamWarps * 32, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int NT, bool kBf16X>
+cudaError_t launch_w4_stream_n(const StreamParams& p, const W4Shape& sh, int grid, size_t smem, cudaStream_t stream) {
+  const bool s16 = sh.scale_bytes == 2;
+  switch (sh.group) {
+    case 32: return s16 ? launch_w4_stream_t<NT, kBf16X, 4, true>(p, grid, smem, stream)
+                        : launch_w4_stream_t<NT, kBf16X, 4, false>(p, grid, smem, stream);
+    case 64: return s16 ? launch_w4_stream_t<NT, kBf16X, 2, true>(p, grid, smem, stream)
+                        : launch_w4_stream_t<NT, kBf16X, 2, false>(p, grid, smem, stream);
+    default: return s16 ? launch_w4_stream_t<NT, kBf16X, 1, true>(p, grid, smem, stream)
+                        : launch_w4_stream_t<NT, kBf16X, 1, false>(p, grid, smem, stream);
+  }
+}
+
+cudaError_t launch_w4_stream(const void* x, bool bf16, int64_t M, const W4Shape& sh, const uint8_t* packed, float* y,
+                             uint32_t* err, cudaStream_t stream, int num_sms) {
+  StreamParams p;
+  p.x = x;
+  p.packed = packed;
+  p.y = y;
+  p.err = err;
+  p.M = (int)M;
+  p.K = (int)sh.K;
+  p.N = sh.N;
+  p.cols = (int)(bf16 ? M : 3 * M);
+  p.blocks = (int)sh.blocks();
+  p.tiles = sh.tiles();
+  const int NT = p.cols <= 8 ? 1 : 2;
+  const size_t smem = w4_stream_smem(NT, p.cols, sh);
+  int64_t per_sm = (227 * 1024) / (int64_t)(smem + 1024);
+  const int most = NT == 1 ? stream_ctas<1>() : stream_ctas<2>();
+  per_sm = per_sm < 1 ? 1 : (per_sm > most ? most : per_sm);
+  const int64_t slots = num_sms * per_sm;
+  const int grid = (int)(p.tiles < slots ? p.tiles : slots);
+  if (bf16)
+    return NT == 1 ? launch_w4_stream_n<1, true>(p, sh, grid, smem, stream)
+                   : launch_w4_stream_n<2, true>(p, sh, grid, smem, stream);
+  return NT == 1 ? launch_w4_stream_n<1, false>(p, sh, grid, smem, stream)
+                 : launch_w4_stream_n<2, false>(p, sh, grid, smem, stream);
 }
 
 int64_t grid_for(int64_t jobs, int64_t per_cta, int num_sms) {
@@ -230,8 +573,16 @@ cudaError_t launch_w4_export(const void* packed, const W4Shape& sh, int8_t* code
   return cudaGetLastError();
 }
 
+bool w4_stream_fits(int64_t M, bool bf16, const W4Shape& sh) {
+  const int64_t cols = bf16 ? M : 3 * M;
+  return cols <= kW4StreamCols && w4_stream_smem(cols <= 8 ? 1 : 2, cols, sh) <= kStreamSmemMax;
+}
+
 cudaError_t launch_forward_w4(const void* x, bool bf16, int64_t M, const W4Shape& sh, const void* packed, float* y,
                               void* ws, cudaStream_t stream, int num_sms) {
+  if (w4_stream_fits(M, bf16, sh))
+    return launch_w4_stream(x, bf16, M, sh, static_cast<const uint8_t*>(packed), y, static_cast<uint32_t*>(ws), stream,
+                            num_sms);
   const cudaError_t e = cudaMemsetAsync(ws, 0, 4, stream);  // the error word
   if (e != cudaSuccess) return e;
   const int grid = (int)grid_for(sh.N * ((M + 3) / 4), 8, num_sms);
