@@ -153,6 +153,8 @@ class BitLinearError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libbitlinear.so once. Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

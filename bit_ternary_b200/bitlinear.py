@@ -9,7 +9,6 @@ the page read out of bounds).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -51,7 +50,8 @@ __all__ = [
 
 
 def _stream_handle(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # The raw handle: torch.cuda.current_stream() would build a Stream object (2 us) around it.
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype) -> None:
@@ -308,11 +308,15 @@ def forward_blocks(x: torch.Tensor, packed: torch.Tensor, D: torch.Tensor,
 _W4_SCALES = {torch.float32: _lib.BL_SCALE_F32, torch.bfloat16: _lib.BL_SCALE_BF16}
 
 
-def _on_device(device: torch.device):
-    """The library launches on the current device: make it the tensors' own."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call_on(device: torch.device, fn: str, *args) -> None:
+    """_lib.call with `device` as the current one (the library launches there)
+    and its current stream as the last argument."""
+    stream = _stream_handle(device)
+    if device.index == torch.cuda.current_device():
+        _lib.call(fn, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _lib.call(fn, *args, stream)
 
 
 def _same_device(t: torch.Tensor, name: str, device: torch.device) -> None:
@@ -336,10 +340,9 @@ class W4Weights:
         self.in_features = K
         self.group = group
         self.scale_dtype = scale_dtype
-
-    @property
-    def scale_type(self) -> int:
-        return _W4_SCALES[self.scale_dtype]
+        self.scale_type = _W4_SCALES[scale_dtype]
+        self.device = data.device
+        self.ptr = data.data_ptr()
 
 
 def _w4_packed_bytes(N: int, K: int, group: int, scale_dtype: torch.dtype) -> int:
@@ -364,9 +367,8 @@ def pack_weights_w4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
     if ws is None:
         ws = _alloc_ws(_lib.lib().bitlinear_pack_workspace_size(N, K), W.device)
     _same_device(ws, "ws", W.device)
-    with _on_device(W.device):
-        _lib.call("bitlinear_pack_weights_w4" + sfx, W.data_ptr(), N, K, group, _W4_SCALES[scale_dtype],
-                  data.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(W.device))
+    _call_on(W.device, "bitlinear_pack_weights_w4" + sfx, W.data_ptr(), N, K, group, _W4_SCALES[scale_dtype],
+             data.data_ptr(), ws.data_ptr(), ws.numel())
     return W4Weights(data, N, K, group, scale_dtype)
 
 
@@ -386,9 +388,8 @@ def import_w4(codes: torch.Tensor, S: torch.Tensor, group: int) -> W4Weights:
     if tuple(S.shape) != (N, -(-K // group)):
         raise ValueError(f"S must have shape [{N}, {-(-K // group)}], got {list(S.shape)}")
     data = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
-    with _on_device(codes.device):
-        _lib.call("bitlinear_w4_import", codes.data_ptr(), S.data_ptr(), N, K, group, _W4_SCALES[S.dtype],
-                  data.data_ptr(), _stream_handle(codes.device))
+    _call_on(codes.device, "bitlinear_w4_import", codes.data_ptr(), S.data_ptr(), N, K, group, _W4_SCALES[S.dtype],
+             data.data_ptr())
     return W4Weights(data, N, K, group, S.dtype)
 
 
@@ -397,9 +398,7 @@ def unpack_w4(w: W4Weights) -> Tuple[torch.Tensor, torch.Tensor]:
     N, K = w.out_features, w.in_features
     codes = torch.empty((N, K), dtype=torch.int8, device=w.data.device)
     S = torch.empty((N, -(-K // w.group)), dtype=w.scale_dtype, device=w.data.device)
-    with _on_device(w.data.device):
-        _lib.call("bitlinear_w4_export", w.data.data_ptr(), N, K, w.group, w.scale_type, codes.data_ptr(),
-                  S.data_ptr(), _stream_handle(w.data.device))
+    _call_on(w.device, "bitlinear_w4_export", w.ptr, N, K, w.group, w.scale_type, codes.data_ptr(), S.data_ptr())
     return codes, S
 
 
@@ -415,7 +414,7 @@ def _w4_input(x: torch.Tensor, w: W4Weights) -> str:
     sfx = _float_input(x, "x")
     if x.dim() != 2 or x.shape[1] != w.in_features:
         raise ValueError(f"x must be [M, {w.in_features}], got {list(x.shape)}")
-    _same_device(x, "x", w.data.device)
+    _same_device(x, "x", w.device)
     return sfx
 
 
@@ -425,17 +424,20 @@ def forward_w4(x: torch.Tensor, w: W4Weights, out: Optional[torch.Tensor] = None
     bf16 (not quantised), y fp32. Calls that can overlap need a workspace each."""
     sfx = _w4_input(x, w)
     M, N, K = x.shape[0], w.out_features, w.in_features
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
-    _need_cuda(y, "out", torch.float32)
-    _same_device(y, "out", x.device)
-    if tuple(y.shape) != (M, N):
-        raise ValueError(f"out must have shape [{M}, {N}], got {list(y.shape)}")
+    if out is None:
+        y = torch.empty(M, N, dtype=torch.float32, device=w.device)
+    else:
+        y = out
+        _need_cuda(y, "out", torch.float32)
+        _same_device(y, "out", w.device)
+        if tuple(y.shape) != (M, N):
+            raise ValueError(f"out must have shape [{M}, {N}], got {list(y.shape)}")
     if ws is None:
-        ws = _alloc_ws(w4_workspace_size(M, N, K), x.device)
-    _same_device(ws, "ws", x.device)
-    with _on_device(x.device):
-        _lib.call("bitlinear_forward_w4" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.data.data_ptr(),
-                  y.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(x.device))
+        ws = _alloc_ws(w4_workspace_size(M, N, K), w.device)
+    else:
+        _same_device(ws, "ws", w.device)
+    _call_on(w.device, "bitlinear_forward_w4" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.ptr,
+             y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
@@ -485,9 +487,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     tokens = torch.empty(B, dtype=torch.int64, device=logits.device)
     logprobs = torch.empty(B, dtype=torch.float32, device=logits.device)
     sfx = "_bf16" if logits.dtype == torch.bfloat16 else ""
-    with _on_device(logits.device):
-        _lib.call("bitlinear_sample" + sfx, logits.data_ptr(), B, V, ld, ctypes.byref(how), u.data_ptr(),
-                  tokens.data_ptr(), logprobs.data_ptr(), _stream_handle(logits.device))
+    _call_on(logits.device, "bitlinear_sample" + sfx, logits.data_ptr(), B, V, ld, ctypes.byref(how), u.data_ptr(),
+             tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs
 
 
@@ -504,10 +505,8 @@ def forward_w4_sample(x: torch.Tensor, w: W4Weights, u: torch.Tensor, temperatur
     if ws is None:
         ws = _alloc_ws(w4_sample_workspace_size(M, N, K), x.device)
     _same_device(ws, "ws", x.device)
-    with _on_device(x.device):
-        _lib.call("bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type,
-                  w.data.data_ptr(), ctypes.byref(how), u.data_ptr(), tokens.data_ptr(), logprobs.data_ptr(),
-                  ws.data_ptr(), ws.numel(), _stream_handle(x.device))
+    _call_on(w.device, "bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.ptr,
+             ctypes.byref(how), u.data_ptr(), tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel())
     return tokens, logprobs
 
 

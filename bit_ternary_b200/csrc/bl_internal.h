@@ -9,6 +9,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 namespace bl {
 
 // Pack workspace: header (the sticky status word at 0, this call's status at
@@ -207,6 +209,9 @@ __device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&pair)[4]) {
 constexpr int kW4StreamCols = 16;
 bool w4_stream_fits(int64_t M, bool bf16, const W4Shape& sh);
 inline size_t ws_w4_bytes(int64_t M, int64_t K) { return kHeaderBytes + align256(6 * (size_t)M * (size_t)K); }
+// The tensor-core kernel for many tokens (bl_w4_gemm.cu).
+cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, const W4Shape& sh, const uint8_t* packed, float* y,
+                           void* ws, cudaStream_t stream, int num_sms);
 // x is fp32, or bf16 bit patterns when bf16.
 cudaError_t launch_forward_w4(const void* x, bool bf16, int64_t M, const W4Shape& sh, const void* packed, float* y,
                               void* ws, cudaStream_t stream, int num_sms);
@@ -225,6 +230,19 @@ struct SampleHow {
 };
 cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, int64_t ld, const SampleHow& how,
                           const float* u, int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms);
+
+// Shared memory beyond 48 KB has to be allowed once per kernel and device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (r == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return r;
+}
 
 cudaError_t launch_selftest_wait(uint32_t* err, uint64_t limit_ns, cudaStream_t stream);
 

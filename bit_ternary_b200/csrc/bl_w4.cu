@@ -8,11 +8,6 @@ namespace bl {
 
 namespace {
 
-__device__ __forceinline__ float w4_scale_load(const uint8_t* p, int i, int scale_bytes) {
-  return scale_bytes == 4 ? reinterpret_cast<const float*>(p)[i]
-                          : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]);
-}
-
 // bf16 nearest to a finite v (half to even), as bits.
 __device__ __forceinline__ uint32_t bf16_rn_bits(float v) {
   const uint32_t b = __float_as_uint(v);
@@ -147,53 +142,6 @@ __global__ void __launch_bounds__(256) w4_export_kernel(const uint8_t* __restric
         static_cast<float*>(S)[dst] = reinterpret_cast<const float*>(sp)[si];
       else
         static_cast<uint16_t*>(S)[dst] = reinterpret_cast<const uint16_t*>(sp)[si];
-    }
-  }
-}
-
-// One warp per output row and up to four tokens: lanes stride over the row's
-// words; a lane's word lies in one group, whose scale multiplies the word's sum.
-template <bool kBf16>
-__global__ void __launch_bounds__(256) w4_plain_kernel(const void* __restrict__ x, int64_t M, const W4Shape sh,
-                                                       const uint8_t* __restrict__ packed, float* __restrict__ y) {
-  const int lane = threadIdx.x & 31;
-  const int64_t words = sh.K / 8;
-  const int64_t mtiles = (M + 3) / 4;
-  const int64_t jobs = sh.N * mtiles;
-  for (int64_t job = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); job < jobs; job += (int64_t)gridDim.x * 8) {
-    const int64_t n = job / mtiles, m0 = (job - n * mtiles) * 4;
-    const int r = (int)(n % kW4Rows);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t wi = lane; wi < words; wi += 32) {
-      const int w = (int)(wi & 15);
-      const uint8_t* blk = packed + w4_block_off(sh, n / kW4Rows, wi >> 4);
-      const uint32_t word = reinterpret_cast<const uint32_t*>(blk)[r * 16 + 4 * (w & 3) + (w >> 2)];
-      const float s = w4_scale_load(blk + kW4CodeBytes, sh.scale_index(r, 8 * w / sh.group), sh.scale_bytes);
-      float c[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = (float)((int)((word >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - 8);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (m0 + i >= M) break;
-        const float4 a = load4<kBf16>(x, ((m0 + i) * sh.K + wi * 8) >> 2);
-        const float4 b = load4<kBf16>(x, (((m0 + i) * sh.K + wi * 8) >> 2) + 1);
-        float t = c[0] * a.x;
-        t = fmaf(c[1], a.y, t);
-        t = fmaf(c[2], a.z, t);
-        t = fmaf(c[3], a.w, t);
-        t = fmaf(c[4], b.x, t);
-        t = fmaf(c[5], b.y, t);
-        t = fmaf(c[6], b.z, t);
-        t = fmaf(c[7], b.w, t);
-        acc[i] = fmaf(s, t, acc[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v = acc[i];
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-      if (lane == 0 && m0 + i < M) y[(m0 + i) * sh.N + n] = v;
     }
   }
 }
@@ -366,6 +314,14 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
   const uint8_t* src = p.packed + (tile0 * p.blocks + b0) * kBlockBytes + 16 * lane;
   const int soff = kW4CodeBytes - 16 * lane + g * (kScaleBytes / 8);
   int64_t left = b1 - b0;
+  // The launch may begin while the one before it still runs. Until that has
+  // ended nothing it may write is read: the first blocks are only asked into L2.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0 && left > 0) {
+    const int n = (int)(left < kDepth ? left : kDepth);
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(n * kBlockBytes) : "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   LaneBlock<GPB, kBf16S> ring[kDepth];
 #pragma unroll
   for (int i = 0; i < kDepth; ++i)
@@ -494,11 +450,21 @@ size_t w4_stream_smem(int NT, int64_t cols, const W4Shape& sh) {
 
 template <int NT, bool kBf16X, int GPB, bool kBf16S>
 cudaError_t launch_w4_stream_t(const StreamParams& p, int grid, size_t smem, cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed{0};
   auto kern = w4_stream_kernel<NT, kBf16X, GPB, kBf16S>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem(kern, kStreamSmemMax, allowed);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kStreamWarps * 32, smem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kStreamWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int NT, bool kBf16X>
@@ -583,15 +549,7 @@ cudaError_t launch_forward_w4(const void* x, bool bf16, int64_t M, const W4Shape
   if (w4_stream_fits(M, bf16, sh))
     return launch_w4_stream(x, bf16, M, sh, static_cast<const uint8_t*>(packed), y, static_cast<uint32_t*>(ws), stream,
                             num_sms);
-  const cudaError_t e = cudaMemsetAsync(ws, 0, 4, stream);  // the error word
-  if (e != cudaSuccess) return e;
-  const int grid = (int)grid_for(sh.N * ((M + 3) / 4), 8, num_sms);
-  const uint8_t* p = static_cast<const uint8_t*>(packed);
-  if (bf16)
-    w4_plain_kernel<true><<<grid, 256, 0, stream>>>(x, M, sh, p, y);
-  else
-    w4_plain_kernel<false><<<grid, 256, 0, stream>>>(x, M, sh, p, y);
-  return cudaGetLastError();
+  return launch_w4_gemm(x, bf16, M, sh, static_cast<const uint8_t*>(packed), y, ws, stream, num_sms);
 }
 
 }  // namespace bl

@@ -1,0 +1,530 @@
+// bl_w4_gemm.cu - the 4-bit group-scale product of many tokens on the 5th-generation
+// tensor cores (tcgen05.mma kind::f16, fp32 accumulators in tensor memory).
+//
+//   y[m,n] = sum_G S[n,G] * (sum over k in G of c[n,k] * x[m,k])
+//
+// Tile: 128 weight rows (MMA M) x BN tokens (MMA N); a stage is 128 columns of
+// K, one block of the packed weights for each of eight row tiles.
+//   A = the codes as bf16 (c * 2^-6, exact), unpacked by four warps from
+//       registers into TMEM (tcgen05.st), a ring of stages.
+//   B = x as bf16, loaded by TMA with 128-byte swizzle: the caller's own bf16 x,
+//       or the three pieces of an fp32 x, which take three MMAs over one A
+//       stage into one accumulator.
+//   D = one group's sum: a scale multiplies sums over its 32, 64 or 128 columns
+//       only, so each group has an accumulator of its own (a ring in TMEM), which
+//       eight drain warps read, multiply by the row's scale and add to the
+//       tile's sums in registers. Scaling the weights instead would round them
+//       to bf16.
+// Warp roles: 0 TMA producer, 1 MMA issuer (TMEM owner), 4..7 unpack, 8..15
+// drain (a warp owns 32 rows x BN / 2 tokens). Every barrier wait is bounded in
+// time; a timeout sets a shared abort flag and the workspace's error word, and
+// all roles run out and exit.
+#include "bl_internal.h"
+
+#include <atomic>
+#include <cstring>
+
+namespace bl {
+
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kStageK = kW4Cols;
+constexpr int kACols = kStageK / 2;  // TMEM columns of an A stage (two bf16 each)
+constexpr uint32_t kTmemCols = 512;
+constexpr int kUnpackWarp0 = 4;
+constexpr int kDrainWarp0 = 8;
+constexpr int kDrainWarps = 8;
+constexpr int kThreads = 32 * (kDrainWarp0 + kDrainWarps);
+constexpr int kAStages = 4;
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <int BN, int PLANES>
+struct Shape {
+  static constexpr int kDBufs = BN == 128 ? 2 : 4;  // group accumulators in flight
+  static constexpr int kACol = kDBufs * BN;
+  static constexpr uint32_t kBoxBytes = BN * 128;   // BN tokens x 64 columns
+  static constexpr uint32_t kBStageBytes = PLANES * 2 * kBoxBytes;
+  static constexpr int kBStages = (int)((200 * 1024) / kBStageBytes) < 6 ? (int)((200 * 1024) / kBStageBytes) : 6;
+  static constexpr int kWarpTokens = BN / 2;
+  static_assert(kACol + kAStages * kACols <= (int)kTmemCols, "TMEM budget");
+  static_assert(kBStages >= 2 && kBoxBytes % 1024 == 0, "shared memory ring");
+};
+
+template <int BN, int PLANES>
+struct Sync {
+  using Sh = Shape<BN, PLANES>;
+  uint64_t full_b[Sh::kBStages];
+  uint64_t empty_b[Sh::kBStages];
+  uint64_t full_a[kAStages];
+  uint64_t empty_a[kAStages];
+  uint64_t acc_full[Sh::kDBufs];
+  uint64_t acc_empty[Sh::kDBufs];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct Params {
+  const uint8_t* packed;
+  float* y;
+  uint32_t* err;
+  int M, K;
+  int64_t N;
+  int64_t row_tiles;  // 16-row tiles of the packed weight
+  int blocks;         // 128-column blocks per row: stages per tile
+  int tiles_n;
+  int num_tiles;
+};
+
+template <int BN, int PLANES>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)Shape<BN, PLANES>::kBStages * Shape<BN, PLANES>::kBStageBytes +
+         ((sizeof(Sync<BN, PLANES>) + 127) & ~size_t(127));
+}
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 operands, fp32 accumulate.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// fp32 accumulator, bf16 A and B, both K-major.
+constexpr uint32_t umma_idesc_bf16(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// acc.xy += v.xy * s.xx (two fp32 multiply-adds)
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, uint64_t ss) {
+  asm("{\n\t.reg .b64 a, v;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 v, {%2, %3};\n\t"
+      "fma.rn.f32x2 a, v, %4, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "r"(v0), "r"(v1), "l"(ss));
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                          uint32_t code) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err, code) ? 1 : 0;
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  return ok != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void ring_next(int& s, uint32_t& ph) {
+  if (++s == N) {
+    s = 0;
+    ph ^= 1;
+  }
+}
+
+template <int BN, int PLANES, int GPB, bool kBf16S>
+__global__ void __launch_bounds__(kThreads, 1)
+    w4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const Params p) {
+  using Sh = Shape<BN, PLANES>;
+  constexpr int kBStages = Sh::kBStages, kDBufs = Sh::kDBufs, kACol = Sh::kACol;
+  constexpr int kBlockBytes = kW4CodeBytes + kW4Rows * GPB * (kBf16S ? 2 : 4);
+  constexpr int kSteps = kStageK / GPB / 16;  // MMAs of one group and piece
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sB = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Sync<BN, PLANES>& S = *reinterpret_cast<Sync<BN, PLANES>*>(sB + (size_t)kBStages * Sh::kBStageBytes);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int my_tiles = p.num_tiles > (int)blockIdx.x ? (p.num_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kBStages; ++s) {
+      mbar_init(&S.full_b[s], 1);
+      mbar_init(&S.empty_b[s], 1);
+    }
+    for (int s = 0; s < kAStages; ++s) {
+      mbar_init(&S.full_a[s], 4);
+      mbar_init(&S.empty_a[s], 1);
+    }
+    for (int b = 0; b < kDBufs; ++b) {
+      mbar_init(&S.acc_full[b], 1);
+      mbar_init(&S.acc_empty[b], kDrainWarps);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(&S.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  volatile int* abort_flag = &S.abort_flag;
+  // The launch may begin while the one before it runs; nothing that one may
+  // write is read before it has ended.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer (x)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int issued = 0;
+      for (int lt = 0; lt < my_tiles; ++lt) {
+        const int tile = blockIdx.x + lt * gridDim.x;
+        const int m0 = (tile / p.tiles_n) * BN;
+        for (int kb = 0; kb < p.blocks; ++kb) {
+          if (!mbar_wait(&S.empty_b[s], ph ^ 1, abort_flag, p.err, kDevTimeoutProducer)) {
+            lt = my_tiles;
+            break;
+          }
+          // Columns past K and tokens past M arrive as zeros.
+          mbar_arrive_expect_tx(&S.full_b[s], Sh::kBStageBytes);
+#pragma unroll
+          for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(sB + (size_t)s * Sh::kBStageBytes + (pl * 2 + h) * Sh::kBoxBytes, &tmap_x,
+                          kb * kStageK + 64 * h, m0, pl, &S.full_b[s]);
+          ++issued;
+          ring_next<kBStages>(s, ph);
+        }
+      }
+      // Let every issued copy land before the CTA can exit.
+      const int first = issued > kBStages ? issued - kBStages : 0;
+      for (int j = first; j < issued; ++j)
+        mbar_wait(&S.full_b[j % kBStages], (j / kBStages) & 1, nullptr, p.err, kDevTimeoutDrain, 100000000ull);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = umma_idesc_bf16(kBM, BN);
+      const uint64_t bdesc0 = umma_sdesc_sw128(sB);
+      int sb = 0, sa = 0, d = 0;
+      uint32_t phb = 0, pha = 0, phd = 0;
+      bool ok = true;
+      const int64_t stages = (int64_t)my_tiles * p.blocks;
+      for (int64_t j = 0; j < stages && ok; ++j) {
+        if (!mbar_wait(&S.full_a[sa], pha, abort_flag, p.err, kDevTimeoutMma) ||
+            !mbar_wait(&S.full_b[sb], phb, abort_flag, p.err, kDevTimeoutMma))
+          break;
+#pragma unroll
+        for (int gi = 0; gi < GPB; ++gi) {
+          if (!mbar_wait(&S.acc_empty[d], phd ^ 1, abort_flag, p.err, kDevTimeoutMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + d * BN;
+#pragma unroll
+          for (int q = 0; q < PLANES; ++q) {
+            const int pl = PLANES - 1 - q;  // the smallest piece first
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              const int ks = gi * kSteps + k;  // 16-column step of the stage
+              const uint64_t bdesc = bdesc0 +
+                                     (uint64_t)((sb * Sh::kBStageBytes + (pl * 2 + (ks >> 2)) * Sh::kBoxBytes) >> 4) +
+                                     2 * (ks & 3);
+              umma_bf16_ts(d_tmem, tmem + kACol + kACols * sa + 8 * ks, bdesc, idesc, (q | k) != 0 ? 1u : 0u);
+            }
+          }
+          tc_commit(&S.acc_full[d]);
+          ring_next<kDBufs>(d, phd);
+        }
+        if (!ok) break;
+        tc_commit(&S.empty_a[sa]);
+        tc_commit(&S.empty_b[sb]);
+        ring_next<kAStages>(sa, pha);
+        ring_next<kBStages>(sb, phb);
+      }
+      // All issued MMAs complete before TMEM is released.
+      tc_commit(&S.drain);
+      mbar_wait(&S.drain, 0, nullptr, p.err, kDevTimeoutDrain, 100000000ull);
+    }
+  } else if (warp >= kUnpackWarp0 && warp < kUnpackWarp0 + 4) {
+    // ------------------------------------------------ unpack: one weight row per thread
+    if (warp == kUnpackWarp0 && lane == 0 && blockIdx.x == 0) *p.err = 0u;
+    const int quarter = warp & 3;  // TMEM lane quarter (hardware rule: warp id % 4)
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    constexpr int kAhead = 3;  // stages of codes in flight
+    const int64_t stages = (int64_t)my_tiles * p.blocks;
+    uint4 buf[kAhead][4];
+    int lt = 0, kb = 0;  // the next stage to load
+    const uint8_t* src = nullptr;
+    const auto load = [&](uint4(&w)[4]) {
+      if (kb == 0) {
+        const int tile = blockIdx.x + lt * gridDim.x;
+        int64_t rt = (int64_t)(tile % p.tiles_n) * (kBM / kW4Rows) + (row / kW4Rows);
+        rt = rt < p.row_tiles ? rt : p.row_tiles - 1;  // rows past the last tile: anything in bounds
+        src = p.packed + rt * p.blocks * kBlockBytes + (row % kW4Rows) * (kStageK / 2);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      src += kBlockBytes;
+      if (++kb == p.blocks) {
+        kb = 0;
+        ++lt;
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (q < stages) load(buf[q]);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t j0 = 0; j0 < stages && ok; j0 += kAhead) {
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int64_t j = j0 + q;
+        if (j >= stages) break;
+        if (!warp_wait(&S.empty_a[s], ph ^ 1, abort_flag, p.err, kDevTimeoutUnpack)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // Word (t, j) of the row holds columns 32 j + 8 t ..: pairs 16 j + 4 t .. of the stage.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t w0 = h == 0 ? buf[q][t].x : buf[q][t].z;
+            const uint32_t w1 = h == 0 ? buf[q][t].y : buf[q][t].w;
+            uint32_t pr[4];
+            w4_unpack(w0, pr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * t + i] = pr[i];
+            w4_unpack(w1, pr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[16 + 4 * t + i] = pr[i];
+          }
+          tmem_st_32x32b_x32(lane_base + kACol + kACols * s + 32 * h, v);
+        }
+        if (j + kAhead < stages) load(buf[q]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.full_a[s]);
+        ring_next<kAStages>(s, ph);
+      }
+    }
+  } else if (warp >= kDrainWarp0) {
+    // ------------------------------------------------ drain: 32 rows x BN / 2 tokens per warp
+    constexpr int kTok = Sh::kWarpTokens;
+    constexpr int kChunk = kTok < 32 ? kTok : 32;
+    const int quarter = warp & 3, half = (warp - kDrainWarp0) >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + half * kTok;
+    const int soff = kW4CodeBytes + ((row & 7) * GPB * 2 + ((row >> 3) & 1)) * (kBf16S ? 2 : 4);
+    int d = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int lt = 0; lt < my_tiles && ok; ++lt) {
+      const int tile = blockIdx.x + lt * gridDim.x;
+      const int m0 = (tile / p.tiles_n) * BN + half * kTok;
+      const int64_t n = (int64_t)(tile % p.tiles_n) * kBM + row;
+      int64_t rt = n / kW4Rows;
+      rt = rt < p.row_tiles ? rt : p.row_tiles - 1;
+      const uint8_t* sp = p.packed + rt * p.blocks * kBlockBytes + soff;
+      const auto scale = [&](int gi) {
+        if (kBf16S) return bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(sp) + 2 * gi));
+        return __ldg(reinterpret_cast<const float*>(sp) + 2 * gi);
+      };
+      float acc[kTok];
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) acc[i] = 0.f;
+      float sc[GPB];
+#pragma unroll
+      for (int gi = 0; gi < GPB; ++gi) sc[gi] = scale(gi);
+      for (int kb = 0; kb < p.blocks && ok; ++kb) {
+        float nsc[GPB];
+        sp += kBlockBytes;
+#pragma unroll
+        for (int gi = 0; gi < GPB; ++gi) nsc[gi] = kb + 1 < p.blocks ? scale(gi) : 0.f;
+#pragma unroll
+        for (int gi = 0; gi < GPB; ++gi) {
+          if (ok && !warp_wait(&S.acc_full[d], ph, abort_flag, p.err, kDevTimeoutEpilogue)) ok = false;
+          if (ok) {
+            tc_fence_after();
+            uint64_t ss;
+            asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(sc[gi]));
+#pragma unroll
+            for (int c = 0; c < kTok; c += kChunk) {
+              uint32_t v[32];
+              if (kChunk == 32) tmem_ld_32x32b_x32(lane_base + d * BN + c, v);
+              else tmem_ld_32x32b_x16(lane_base + d * BN + c, v);
+              tmem_wait_ld();
+              if (c + kChunk == kTok) {  // all of it is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.acc_empty[d]);
+              }
+#pragma unroll
+              for (int i = 0; i < kChunk; i += 2) fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], ss);
+            }
+            ring_next<kDBufs>(d, ph);
+          }
+        }
+#pragma unroll
+        for (int gi = 0; gi < GPB; ++gi) sc[gi] = nsc[gi];
+      }
+      if (ok && n < p.N) {
+        float* out = p.y + (int64_t)m0 * p.N + n;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+          if (m0 + i < p.M) __stcs(out, acc[i] * kW4Unit);
+          out += p.N;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// The three bf16 pieces of an fp32 x [M, K], planes [3][M][K].
+__global__ void __launch_bounds__(256) w4_split_kernel(const float4* __restrict__ x, int64_t n4, uint2* planes) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    const float4 v = x[i];
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split_bf16x3(f[j], h[j], m[j], l[j]);
+    planes[i] = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    planes[n4 + i] = make_uint2(m[0] | (m[1] << 16), m[2] | (m[3] << 16));
+    planes[2 * n4 + i] = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+  }
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_dependent(Kernel kern, int grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int BN, int PLANES, int GPB, bool kBf16S>
+cudaError_t launch_t(const CUtensorMap& tx, const Params& p, int grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed{0};
+  auto kern = w4_gemm_kernel<BN, PLANES, GPB, kBf16S>;
+  constexpr size_t smem = smem_bytes<BN, PLANES>();
+  static_assert(smem <= kSmemMax, "shared memory");
+  const cudaError_t e = allow_smem(kern, smem, allowed);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, grid, kThreads, smem, stream, tx, p);
+}
+
+template <int BN, int PLANES>
+cudaError_t launch_n(const CUtensorMap& tx, const Params& p, const W4Shape& sh, int grid, cudaStream_t stream) {
+  const bool s16 = sh.scale_bytes == 2;
+  switch (sh.group) {
+    case 32: return s16 ? launch_t<BN, PLANES, 4, true>(tx, p, grid, stream)
+                        : launch_t<BN, PLANES, 4, false>(tx, p, grid, stream);
+    case 64: return s16 ? launch_t<BN, PLANES, 2, true>(tx, p, grid, stream)
+                        : launch_t<BN, PLANES, 2, false>(tx, p, grid, stream);
+    default: return s16 ? launch_t<BN, PLANES, 1, true>(tx, p, grid, stream)
+                        : launch_t<BN, PLANES, 1, false>(tx, p, grid, stream);
+  }
+}
+
+// Estimated cycles of a launch with BN-token tiles: waves of tiles times a
+// tile's stages, each as long as its MMAs, its unpacking or its drains.
+int64_t estimate(int BN, int planes, int gpb, int64_t M, int64_t tiles_n, int64_t blocks, int sms) {
+  const int64_t tiles = (M + BN - 1) / BN * tiles_n;
+  const int64_t waves = (tiles + sms - 1) / sms;
+  const int64_t mma = (int64_t)planes * 8 * (BN / 2);
+  const int64_t drain = (int64_t)gpb * (BN + 60);
+  int64_t stage = mma > drain ? mma : drain;
+  stage = stage > 260 ? stage : 260;
+  return waves * (blocks * stage + 1500);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, const W4Shape& sh, const uint8_t* packed, float* y,
+                           void* ws, cudaStream_t stream, int num_sms) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const int planes = bf16 ? 1 : 3;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  void* xb = const_cast<void*>(x);
+  if (!bf16) {
+    xb = base + kHeaderBytes;
+    const int64_t n4 = M * sh.K / 4;
+    const int64_t want = (n4 + 255) / 256, most = (int64_t)num_sms * 8;
+    const cudaError_t e =
+        launch_dependent(w4_split_kernel, (int)(want < most ? want : most), 256, 0, stream,
+                         static_cast<const float4*>(x), n4, static_cast<uint2*>(xb));
+    if (e != cudaSuccess) return e;
+  }
+  Params p;
+  p.packed = packed;
+  p.y = y;
+  p.err = reinterpret_cast<uint32_t*>(base);
+  p.M = (int)M;
+  p.K = (int)sh.K;
+  p.N = sh.N;
+  p.row_tiles = sh.tiles();
+  p.blocks = (int)sh.blocks();
+  const int64_t tiles_n = (sh.N + kBM - 1) / kBM;
+  p.tiles_n = (int)tiles_n;
+  const int gpb = kW4Cols / sh.group;
+  int BN = 32;
+  for (const int cand : {64, 128})
+    if (estimate(cand, planes, gpb, M, tiles_n, p.blocks, num_sms) <
+        estimate(BN, planes, gpb, M, tiles_n, p.blocks, num_sms))
+      BN = cand;
+  const int64_t nt = (M + BN - 1) / BN * tiles_n;
+  if (nt > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  p.num_tiles = (int)nt;
+  CUtensorMap tx;
+  const cuuint64_t gdim[3] = {(cuuint64_t)sh.K, (cuuint64_t)M, (cuuint64_t)planes};
+  const cuuint64_t gstride[2] = {(cuuint64_t)sh.K * 2, (cuuint64_t)sh.K * 2 * (cuuint64_t)M};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)BN, 1u};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  if (encode(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, xb, gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const int grid = (int)(nt < num_sms ? nt : num_sms);
+  if (planes == 1) {
+    if (BN == 32) return launch_n<32, 1>(tx, p, sh, grid, stream);
+    return BN == 64 ? launch_n<64, 1>(tx, p, sh, grid, stream) : launch_n<128, 1>(tx, p, sh, grid, stream);
+  }
+  if (BN == 32) return launch_n<32, 3>(tx, p, sh, grid, stream);
+  return BN == 64 ? launch_n<64, 3>(tx, p, sh, grid, stream) : launch_n<128, 3>(tx, p, sh, grid, stream);
+}
+
+}  // namespace bl
