@@ -15,7 +15,7 @@
 //       eight drain warps read, multiply by the row's scale and add to the
 //       tile's sums in registers. Scaling the weights instead would round them
 //       to bf16.
-// Warp roles: 0 TMA producer, 1 MMA issuer (TMEM owner), 4..7 unpack, 8..15
+// Warp roles: 0 TMA producer (TMEM owner), 1 MMA issuer, 4..7 unpack, 8..15
 // drain (a warp owns 32 rows x BN / 2 tokens). Every barrier wait is bounded in
 // time; a timeout sets a shared abort flag and the workspace's error word, and
 // all roles run out and exit.
@@ -36,12 +36,12 @@ constexpr int kUnpackWarp0 = 4;
 constexpr int kDrainWarp0 = 8;
 constexpr int kDrainWarps = 8;
 constexpr int kThreads = 32 * (kDrainWarp0 + kDrainWarps);
-constexpr int kAStages = 4;
 constexpr size_t kSmemMax = 227 * 1024;
 
 template <int BN, int PLANES>
 struct Shape {
-  static constexpr int kDBufs = BN == 128 ? 2 : 4;  // group accumulators in flight
+  static constexpr int kDBufs = BN == 128 ? 3 : 4;  // group accumulators in flight
+  static constexpr int kAStages = BN == 128 ? 2 : 4;
   static constexpr int kACol = kDBufs * BN;
   static constexpr uint32_t kBoxBytes = BN * 128;   // BN tokens x 64 columns
   static constexpr uint32_t kBStageBytes = PLANES * 2 * kBoxBytes;
@@ -56,8 +56,8 @@ struct Sync {
   using Sh = Shape<BN, PLANES>;
   uint64_t full_b[Sh::kBStages];
   uint64_t empty_b[Sh::kBStages];
-  uint64_t full_a[kAStages];
-  uint64_t empty_a[kAStages];
+  uint64_t full_a[Sh::kAStages];
+  uint64_t empty_a[Sh::kAStages];
   uint64_t acc_full[Sh::kDBufs];
   uint64_t acc_empty[Sh::kDBufs];
   uint64_t drain;
@@ -119,12 +119,62 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t
       : "r"(v0), "r"(v1), "l"(ss));
 }
 
+// 16, 32 or 64 consecutive TMEM columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+        "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+        "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+        "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The whole warp waits; the outcome is warp-uniform.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
                                           uint32_t code) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err, code) ? 1 : 0;
   ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
   return ok != 0;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 template <int N>
@@ -139,14 +189,15 @@ template <int BN, int PLANES, int GPB, bool kBf16S>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const Params p) {
   using Sh = Shape<BN, PLANES>;
-  constexpr int kBStages = Sh::kBStages, kDBufs = Sh::kDBufs, kACol = Sh::kACol;
+  constexpr int kBStages = Sh::kBStages, kAStages = Sh::kAStages, kDBufs = Sh::kDBufs, kACol = Sh::kACol;
   constexpr int kBlockBytes = kW4CodeBytes + kW4Rows * GPB * (kBf16S ? 2 : 4);
   constexpr int kSteps = kStageK / GPB / 16;  // MMAs of one group and piece
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sB = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Sync<BN, PLANES>& S = *reinterpret_cast<Sync<BN, PLANES>*>(sB + (size_t)kBStages * Sh::kBStageBytes);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Warp-uniform by construction, so that what follows from it stays in uniform registers.
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int my_tiles = p.num_tiles > (int)blockIdx.x ? (p.num_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
   if (threadIdx.x == 0) {
@@ -167,98 +218,125 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     tma_prefetch_desc(&tmap_x);
   }
-  if (warp == 1) {
+  if (warp == 0) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = S.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem_base, 0);
   volatile int* abort_flag = &S.abort_flag;
   // The launch may begin while the one before it runs; nothing that one may
   // write is read before it has ended.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 0) {
-    // ------------------------------------------------ TMA producer (x)
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int issued = 0;
-      for (int lt = 0; lt < my_tiles; ++lt) {
-        const int tile = blockIdx.x + lt * gridDim.x;
-        const int m0 = (tile / p.tiles_n) * BN;
-        for (int kb = 0; kb < p.blocks; ++kb) {
-          if (!mbar_wait(&S.empty_b[s], ph ^ 1, abort_flag, p.err, kDevTimeoutProducer)) {
-            lt = my_tiles;
-            break;
+  // 128 registers a thread at launch, shared out anew among the four groups of
+  // four warps: 40 + 120 + 176 + 176 = 512.
+  if (warp < kUnpackWarp0) {
+    regs_down<40>();
+    if (warp == 0) {
+      // ------------------------------------------------ TMA producer (x)
+      if (lane == 0) {
+        int s = 0;
+        uint32_t ph = 0;
+        int issued = 0;
+        for (int lt = 0; lt < my_tiles; ++lt) {
+          const int tile = blockIdx.x + lt * gridDim.x;
+          const int m0 = (tile / p.tiles_n) * BN;
+          for (int kb = 0; kb < p.blocks; ++kb) {
+            if (!mbar_wait(&S.empty_b[s], ph ^ 1, abort_flag, p.err, kDevTimeoutProducer)) {
+              lt = my_tiles;
+              break;
+            }
+            // Columns past K and tokens past M arrive as zeros.
+            mbar_arrive_expect_tx(&S.full_b[s], Sh::kBStageBytes);
+#pragma unroll
+            for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                tma_load_3d(sB + (size_t)s * Sh::kBStageBytes + (pl * 2 + h) * Sh::kBoxBytes, &tmap_x,
+                            kb * kStageK + 64 * h, m0, pl, &S.full_b[s]);
+            ++issued;
+            ring_next<kBStages>(s, ph);
           }
-          // Columns past K and tokens past M arrive as zeros.
-          mbar_arrive_expect_tx(&S.full_b[s], Sh::kBStageBytes);
-#pragma unroll
-          for (int pl = 0; pl < PLANES; ++pl)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(sB + (size_t)s * Sh::kBStageBytes + (pl * 2 + h) * Sh::kBoxBytes, &tmap_x,
-                          kb * kStageK + 64 * h, m0, pl, &S.full_b[s]);
-          ++issued;
-          ring_next<kBStages>(s, ph);
         }
+        // Let every issued copy land before the CTA can exit.
+        const int first = issued > kBStages ? issued - kBStages : 0;
+        for (int j = first; j < issued; ++j)
+          mbar_wait(&S.full_b[j % kBStages], (j / kBStages) & 1, nullptr, p.err, kDevTimeoutDrain, 100000000ull);
       }
-      // Let every issued copy land before the CTA can exit.
-      const int first = issued > kBStages ? issued - kBStages : 0;
-      for (int j = first; j < issued; ++j)
-        mbar_wait(&S.full_b[j % kBStages], (j / kBStages) & 1, nullptr, p.err, kDevTimeoutDrain, 100000000ull);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    } else if (warp == 1) {
+      // ------------------------------------------------ MMA issuer
+      // The whole warp walks the groups and one lane issues: addresses and
+      // descriptors stay in uniform registers, as the instruction wants them. A
+      // lane of its own (a divergent branch) needed 135 cycles an MMA for the
+      // moves, where 128 tokens take the tensor pipe 64. The barriers of the next
+      // group are looked at before the last MMAs of this one are issued: waiting
+      // for them in turn took 450 cycles a stage, which the pipe's queue (a few
+      // MMAs) does not cover.
       const uint32_t idesc = umma_idesc_bf16(kBM, BN);
       const uint64_t bdesc0 = umma_sdesc_sw128(sB);
       int sb = 0, sa = 0, d = 0;
       uint32_t phb = 0, pha = 0, phd = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       const int64_t stages = (int64_t)my_tiles * p.blocks;
       for (int64_t j = 0; j < stages && ok; ++j) {
-        if (!mbar_wait(&S.full_a[sa], pha, abort_flag, p.err, kDevTimeoutMma) ||
-            !mbar_wait(&S.full_b[sb], phb, abort_flag, p.err, kDevTimeoutMma))
-          break;
+        const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (int)(Sh::kBStageBytes >> 4));
+        const uint32_t a_tmem = tmem + kACol + kACols * sa;
+        const int sa0 = sa, sb0 = sb;
 #pragma unroll
         for (int gi = 0; gi < GPB; ++gi) {
-          if (!mbar_wait(&S.acc_empty[d], phd ^ 1, abort_flag, p.err, kDevTimeoutMma)) {
-            ok = false;
-            break;
+          if (!ready) {
+            ok = (gi != 0 || (warp_wait(&S.full_a[sa0], pha, abort_flag, p.err, kDevTimeoutMma) &&
+                              warp_wait(&S.full_b[sb0], phb, abort_flag, p.err, kDevTimeoutMma))) &&
+                 warp_wait(&S.acc_empty[d], phd ^ 1, abort_flag, p.err, kDevTimeoutMma);
+            if (!ok) break;
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem + d * BN;
+          const int d0 = d;
+          ring_next<kDBufs>(d, phd);
+          if (gi == GPB - 1) {
+            ring_next<kAStages>(sa, pha);
+            ring_next<kBStages>(sb, phb);
+          }
+          bool seen = false;
+          if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < PLANES; ++q) {
-            const int pl = PLANES - 1 - q;  // the smallest piece first
+            for (int q = 0; q < PLANES; ++q) {
+              const int pl = PLANES - 1 - q;  // the smallest piece first
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              const int ks = gi * kSteps + k;  // 16-column step of the stage
-              const uint64_t bdesc = bdesc0 +
-                                     (uint64_t)((sb * Sh::kBStageBytes + (pl * 2 + (ks >> 2)) * Sh::kBoxBytes) >> 4) +
-                                     2 * (ks & 3);
-              umma_bf16_ts(d_tmem, tmem + kACol + kACols * sa + 8 * ks, bdesc, idesc, (q | k) != 0 ? 1u : 0u);
+              for (int k = 0; k < kSteps; ++k) {
+                if (q * kSteps + k == PLANES * kSteps - 2) {
+                  seen = mbar_test(&S.acc_empty[d], phd ^ 1);
+                  if (gi == GPB - 1) seen = seen & mbar_test(&S.full_a[sa], pha) & mbar_test(&S.full_b[sb], phb);
+                }
+                const int ks = gi * kSteps + k;  // 16-column step of the stage
+                umma_bf16_ts(d_tmem, a_tmem + 8 * ks,
+                             bdesc + (uint64_t)((pl * 2 + (ks >> 2)) * (int)(Sh::kBoxBytes >> 4) + 2 * (ks & 3)), idesc,
+                             (q | k) != 0 ? 1u : 0u);
+              }
+            }
+            tc_commit(&S.acc_full[d0]);
+            if (gi == GPB - 1) {
+              tc_commit(&S.empty_a[sa0]);
+              tc_commit(&S.empty_b[sb0]);
             }
           }
-          tc_commit(&S.acc_full[d]);
-          ring_next<kDBufs>(d, phd);
+          ready = __any_sync(0xFFFFFFFFu, seen);
         }
-        if (!ok) break;
-        tc_commit(&S.empty_a[sa]);
-        tc_commit(&S.empty_b[sb]);
-        ring_next<kAStages>(sa, pha);
-        ring_next<kBStages>(sb, phb);
       }
       // All issued MMAs complete before TMEM is released.
-      tc_commit(&S.drain);
-      mbar_wait(&S.drain, 0, nullptr, p.err, kDevTimeoutDrain, 100000000ull);
+      if (elect_one()) {
+        tc_commit(&S.drain);
+        mbar_wait(&S.drain, 0, nullptr, p.err, kDevTimeoutDrain, 100000000ull);
+      }
+      __syncwarp();
     }
-  } else if (warp >= kUnpackWarp0 && warp < kUnpackWarp0 + 4) {
+  } else if (warp < kDrainWarp0) {
     // ------------------------------------------------ unpack: one weight row per thread
+    regs_down<120>();
     if (warp == kUnpackWarp0 && lane == 0 && blockIdx.x == 0) *p.err = 0u;
     const int quarter = warp & 3;  // TMEM lane quarter (hardware rule: warp id % 4)
     const int row = quarter * 32 + lane;
@@ -325,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_next<kAStages>(s, ph);
       }
     }
-  } else if (warp >= kDrainWarp0) {
+  } else {
     // ------------------------------------------------ drain: 32 rows x BN / 2 tokens per warp
+    regs_up<176>();
     constexpr int kTok = Sh::kWarpTokens;
-    constexpr int kChunk = kTok < 32 ? kTok : 32;
     const int quarter = warp & 3, half = (warp - kDrainWarp0) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + half * kTok;
@@ -365,20 +443,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             uint64_t ss;
             asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(sc[gi]));
+            uint32_t v[kTok];
+            tmem_ld_cols(lane_base + d * BN, v);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.acc_empty[d]);  // all of it is in registers
 #pragma unroll
-            for (int c = 0; c < kTok; c += kChunk) {
-              uint32_t v[32];
-              if (kChunk == 32) tmem_ld_32x32b_x32(lane_base + d * BN + c, v);
-              else tmem_ld_32x32b_x16(lane_base + d * BN + c, v);
-              tmem_wait_ld();
-              if (c + kChunk == kTok) {  // all of it is in registers
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.acc_empty[d]);
-              }
-#pragma unroll
-              for (int i = 0; i < kChunk; i += 2) fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], ss);
-            }
+            for (int i = 0; i < kTok; i += 2) fma2(acc[i], acc[i + 1], v[i], v[i + 1], ss);
             ring_next<kDBufs>(d, ph);
           }
         }
@@ -398,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
