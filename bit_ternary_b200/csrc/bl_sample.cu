@@ -5,18 +5,15 @@
 // 64-bit integers (V <= 2^22 keeps a row's sum below 2^62), so every sum is
 // exact and no order of adding changes the token.
 //
-// A cluster of 1 to 8 CTAs owns a row: each CTA reads its stretch once into
-// shared memory as ordered 32-bit keys, and every later pass runs there. The
-// thresholds of top-k and top-p come from one histogram of 2048 bins, linear in
-// x, of one 32-bit atomic per token: a count and the sum of the tokens' sixteenths
-// of a bin. Counts place the k-th token in a bin exactly; the sixteenths bound
-// every bin's weight to about 0.1%, which places the border of top-p within a
-// bin or two without an exponential. The tokens of those bins (some hundreds)
-// are sorted and settle the border exactly. Top-p then needs one exponential
-// per token for the exact sum, a draw without filters likewise, top-k none
-// beyond the kept tokens. What bounds it: the exponentials' 64-bit arithmetic
-// (ten instructions a token) for large batches, the cluster barriers (five to
-// seven of about a microsecond) for a single row.
+// A cluster of 1 to 16 CTAs owns a row: each CTA reads its stretch once into
+// shared memory, and every later pass runs there. The thresholds of top-k and
+// top-p come from one histogram of 2048 bins, linear in x, of one 32-bit atomic
+// per token: a count and the sum of the tokens' sixteenths of a bin. Counts place
+// the k-th token in a bin exactly; the sixteenths bound every bin's weight to
+// about 0.1%, which places the border of top-p within a bin or two without an
+// exponential. The tokens of those bins (some hundreds) are sorted and settle
+// the border exactly. Top-p then needs one exponential per token for the exact
+// sum, a draw without filters likewise, top-k none beyond the kept tokens.
 #include "bl_internal.h"
 
 #include <cstddef>
@@ -29,7 +26,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;          // the last one holds what lies past the range
 constexpr int kListMax = 2048;       // tokens that a list of candidates holds
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kPackMax = 16383;      // tokens per CTA whose count and sixteenths fit 14 + 18 bits
 constexpr size_t kSampleSmemMax = 225 * 1024;
 constexpr double kWeightOne = 1099511627776.0;  // 2^40
@@ -49,7 +46,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// Shared memory of a CTA; the keys follow it. Every member starts on a 16-byte
+// Shared memory of a CTA; the logits follow it. Every member starts on a 16-byte
 // boundary. Two regions serve twice: the
 // leader's totals hold the candidates once a border's bins are known, its
 // histogram their weights.
@@ -63,18 +60,29 @@ struct alignas(16) Smem {
   };
   union {
     uint32_t hist[kBins];    // this CTA: count << 18 | sixteenths, or counts
-    u64 wlist[kListMax];
+    u64 local[kListMax];     // this CTA's candidates, on their way to the leader
+    u64 wlist[kListMax];     // leader: weights of the list
   };
   alignas(16) double tab[256];           // 2^(40 + j / 256)
-  alignas(16) u64 red[kWarps];
-  alignas(16) double redd[2][kWarps];
+  alignas(16) u64 red[3][kWarps];
+  alignas(16) float redf[2][kWarps];
+  int bin_lo, bin_hi;        // leader: bins of top-p's candidates
   alignas(16) u64 xch[2][kMaxCluster][4];  // what the CTAs of the cluster tell one another
-  alignas(16) int list_n;                // leader
+  alignas(16) uint32_t list_n;           // leader
+  uint32_t local_n, base;    // this CTA's candidates, and where they go in the list
   // Broadcast by the leader.
-  int g_lo, g_hi;            // bins to collect
+  uint32_t mode;
+  uint32_t hi_key, lo_key;   // candidates: lo_key <= key < hi_key
   uint32_t cut;              // kept: key > cut, and the first `ties` with key == cut
-  u64 ties;
-  int cut_partial;           // more tokens than `ties` have that key
+  uint32_t cut_partial;      // more tokens than `ties` have that key
+  alignas(8) u64 ties;
+};
+// What the leader makes of a histogram.
+enum : uint32_t {
+  kWhole,   // the candidates are all that can stay: draw from the list
+  kBorder,  // the candidates hold the border
+  kCrowd,   // more of them than a list holds
+  kZeros,   // only tokens of weight zero are in question
 };
 static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, xch) % 16 == 0, "alignment");
 
@@ -94,6 +102,9 @@ __device__ __forceinline__ uint32_t remote_add(uint32_t a, uint32_t v) {
   uint32_t old;
   asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
   return old;
+}
+__device__ __forceinline__ void remote_red(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -115,28 +126,47 @@ struct Row {
 
 // exp((x - max) / T) in units of 2^-40, by a table of 2^(j/256) and a cubic
 // (P. T. P. Tang, ACM TOMS 15(2), 1989): within 2^-42 relative before rounding.
-__device__ __forceinline__ u64 key_weight(uint32_t key, const Row& r, const double* tab) {
-  if (key == r.top) return 1ull << 40;
-  if (key == 0u || r.mxf == INFINITY) return 0ull;
-  double t = (r.mx - (double)key_value(key)) * r.c;
+// The result is 2^52 + w as a double's bits: kMagicBits less is w, and sums of
+// such bits, modulo 2^64, are sums of weights and counts of kMagicBits.
+constexpr u64 kMagicBits = 0x4330000000000000ull;  // 2^52
+__device__ __forceinline__ u64 weight_bits(float x, const Row& r, const double* tab) {
+  double t = (r.mx - (double)x) * r.c;
   t = fmax(t, -256.0 * 64.0);
   const double magic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
   const double tm = t + magic;
   const int n = __double2loint(tm);
-  const double rho = (t - (tm - magic)) * (0.693147180559945309417 / 256.0);
-  const double q = rho * fma(rho, fma(rho, 1.0 / 6.0, 0.5), 1.0);
+  const double f = t - (tm - magic);
+  constexpr double ln = 0.693147180559945309417 / 256.0;
+  const double q = f * fma(f, fma(f, ln * ln * ln / 6.0, ln * ln / 2.0), ln);
   double v = tab[n & 255];
   v = fma(v, q, v);
-  v = __hiloint2double(__double2hiint(v) + (n >> 8) * (1 << 20), __double2loint(v));  // times 2^(n >> 8)
-  const double vm = v + 4503599627370496.0;  // 2^52: the integer nearest to v in the low bits
-  return ((u64)(uint32_t)(__double2hiint(vm) & 0x000FFFFF) << 32) | (uint32_t)__double2loint(vm);
+  v = __hiloint2double(__double2hiint(v) + ((n & ~255) << 12), __double2loint(v));  // times 2^(n >> 8)
+  return (u64)__double_as_longlong(v + 4503599627370496.0);
+}
+__device__ __forceinline__ u64 weight(float x, const Row& r, const double* tab) {
+  if (x == r.mxf) return 1ull << 40;
+  if (!(x > -INFINITY) || r.mxf == INFINITY) return 0ull;
+  return weight_bits(x, r, tab) - kMagicBits;
+}
+__device__ __forceinline__ u64 key_weight(uint32_t key, const Row& r, const double* tab) {
+  return weight(key_value(key), r, tab);
 }
 
 // Sixteenths of a bin from the largest logit; monotone in x.
-__device__ __forceinline__ uint32_t bin16(uint32_t key, const Row& r) {
-  if (key == r.top) return 0u;
-  const float pos = fminf((r.mxf - key_value(key)) * r.scale, (float)(kBins - 1));
+__device__ __forceinline__ uint32_t bin16(float x, const Row& r) {
+  if (x == r.mxf) return 0u;
+  const float pos = fminf((r.mxf - x) * r.scale, (float)(kBins - 1));
   return (uint32_t)__float_as_int(fmaf(pos, 16.0f, 8388608.0f)) & 0x7FFFFFu;  // 2^23: rounds to an integer
+}
+// The smallest key whose token lies before bin `bin` (bin > 0).
+__device__ __forceinline__ uint32_t bin_key(uint32_t bin, const Row& r) {
+  uint32_t lo = 0u, hi = r.top;  // the largest logit lies in bin 0
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2u;
+    if (mid > 0x007FFFFFu && (bin16(key_value(mid), r) >> 4) < bin) hi = mid;  // smaller keys are -inf or NaN
+    else lo = mid + 1u;
+  }
+  return lo;
 }
 
 template <typename T>
@@ -156,12 +186,12 @@ __device__ __forceinline__ u64 block_scan(u64 v, Smem& s, u64& all) {
     if (lane >= d) inc += o;
   }
   __syncthreads();
-  if (lane == 31) s.red[warp] = inc;
+  if (lane == 31) s.red[0][warp] = inc;
   __syncthreads();
   u64 before = 0, t = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
-    const u64 x = s.red[i];
+    const u64 x = s.red[0][i];
     if (i < warp) before += x;
     t += x;
   }
@@ -169,11 +199,13 @@ __device__ __forceinline__ u64 block_scan(u64 v, Smem& s, u64& all) {
   return before + inc - v;
 }
 
-// Sorts the first 2^k >= n entries of `a` (zeros or ones past n, whichever
-// belongs last), largest first or smallest first.
+// Sorts n entries of `a` (bitonic, padded to a power of two), largest first or
+// smallest first. A warp's 32 pairs of a stage lie in 64 entries of its own
+// while partners are at most 32 apart: those stages need no block barrier.
 __device__ __forceinline__ void block_sort(u64* a, int n, bool descending) {
-  int p = 2;
+  int p = 64;
   while (p < n) p <<= 1;
+  __syncthreads();
   for (int i = n + threadIdx.x; i < p; i += kThreads) a[i] = descending ? 0ull : ~0ull;
   __syncthreads();
   for (int k = 2; k <= p; k <<= 1) {
@@ -187,9 +219,12 @@ __device__ __forceinline__ void block_sort(u64* a, int n, bool descending) {
           a[hi] = x;
         }
       }
-      __syncthreads();
+      const int next = j > 1 ? j >> 1 : k;
+      if (j > 32 || next > 32) __syncthreads();
+      else __syncwarp();
     }
   }
+  __syncthreads();
 }
 
 struct SampleParams {
@@ -207,18 +242,77 @@ template <bool kBf16, bool kResident>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(128) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
-  uint32_t* skey = reinterpret_cast<uint32_t*>(raw + sizeof(Smem));
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);  // clusters are runs of C blocks
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int64_t b = blockIdx.x / C;
   const int64_t i0 = (int64_t)rank * p.per;
   const int64_t rest = p.V - i0;
   const int n = rest <= 0 ? 0 : (rest < p.per ? (int)rest : p.per);
-  const uint32_t lead_cnt = remote_addr(s.total.cnt, 0), lead_off = remote_addr(s.total.off, 0);
-  const uint32_t lead_list = remote_addr(s.list, 0), lead_n = remote_addr(&s.list_n, 0);
   // Another CTA's shared memory may be touched once it has begun: waited for
   // below, before the first exchange.
   cluster_arrive();
+
+  // ---- the row, once: logits (NaN as -inf, -0 as 0), their extremes, how many are in
+  const char* row = static_cast<const char*>(p.logits) + (b * p.ld + i0) * (kBf16 ? 2 : 4);
+  const auto clean = [](float x) { return fmaxf(x, -INFINITY) + 0.0f; };
+  const auto load = [&](int i) {
+    return clean(kBf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row)[i])
+                       : reinterpret_cast<const float*>(row)[i]);
+  };
+  // Element i sits at data[i]: shifted so that 16-byte pieces of the row stay 16-byte pieces.
+  constexpr int kVec = kBf16 ? 8 : 4;
+  const int shift = (int)((reinterpret_cast<uintptr_t>(row) / (kBf16 ? 2 : 4)) & (kVec - 1));
+  float* const base = reinterpret_cast<float*>(raw + sizeof(Smem));
+  float* const data = base + shift;
+  const auto at = [&](int i) { return kResident ? data[i] : load(i); };
+  float fmx = -INFINITY, fmn = INFINITY;
+  uint32_t valid = 0u;
+  const auto note = [&](float x) {
+    fmx = fmaxf(fmx, x);
+    if (x > -INFINITY) {
+      fmn = fminf(fmn, x);
+      ++valid;
+    }
+  };
+  if (kResident) {
+    const int pieces = (n + shift + kVec - 1) / kVec;
+    constexpr int kLoads = kBf16 ? 4 : 8;
+    for (int v0 = tid; v0 < pieces; v0 += kThreads * kLoads) {
+      uint4 q[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int v = v0 + j * kThreads, e = v * kVec - shift;
+        if (v < pieces && e >= 0 && e + kVec <= n)
+          q[j] = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)e * (kBf16 ? 2 : 4)));
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int v = v0 + j * kThreads, e = v * kVec - shift;
+        if (v >= pieces) break;
+        if (e >= 0 && e + kVec <= n) {
+          const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+          float f[kVec];
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            f[i] = clean(kBf16 ? __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16)
+                               : __uint_as_float(w[i & 3]));
+            note(f[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kVec; i += 4)
+            *reinterpret_cast<float4*>(base + v * kVec + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        } else {  // the ragged ends
+          for (int i = e < 0 ? 0 : e; i < e + kVec && i < n; ++i) {
+            const float x = load(i);
+            data[i] = x;
+            note(x);
+          }
+        }
+      }
+    }
+  } else {
+    for (int i = tid; i < n; i += kThreads) note(load(i));
+  }
 
   // ---- settings of the row
   const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;
@@ -230,35 +324,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const double pp = pset > 0.0f ? (double)pset : 0.0;
   const u64 wmin = mset > 0.0f ? (u64)ceil((mset < 1.0f ? (double)mset : 1.0) * kWeightOne) : 0ull;
 
-  // ---- the row, once: keys, their largest and smallest, how many are in
-  const char* row = static_cast<const char*>(p.logits) + (b * p.ld + i0) * (kBf16 ? 2 : 4);
-  const auto load = [&](int i) {
-    return sample_key(kBf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row)[i])
-                            : reinterpret_cast<const float*>(row)[i]);
-  };
-  const auto key_at = [&](int i) { return kResident ? skey[i] : load(i); };
-  uint32_t kmax = 0u, kmin = 0xFFFFFFFFu, valid32 = 0u;
-  constexpr int kLoads = 8;
-  for (int base = tid; base < n; base += kThreads * kLoads) {
-    uint32_t k8[kLoads];
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) k8[j] = base + j * kThreads < n ? load(base + j * kThreads) : 0u;
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      if (kResident && base + j * kThreads < n) skey[base + j * kThreads] = k8[j];
-      kmax = max(kmax, k8[j]);
-      if (k8[j] != 0u) {
-        kmin = min(kmin, k8[j]);
-        ++valid32;
-      }
-    }
-  }
   for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
-  if (rank == 0) {
+  if (rank == 0)
     for (int i = tid; i < kBins; i += kThreads) s.total.cnt[i] = s.total.off[i] = 0u;
-    if (tid == 0) s.list_n = 0;
-  }
+  if (tid == 0) s.list_n = s.local_n = 0u;
   if (tid < 256) s.tab[tid] = exp2(40.0 + tid * (1.0 / 256.0));
+  const uint32_t lead_cnt = remote_addr(s.total.cnt, 0), lead_off = remote_addr(s.total.off, 0);
+  const uint32_t lead_list = remote_addr(s.list, 0), lead_n = remote_addr(&s.list_n, 0);
 
   // Three values of every CTA to all CTAs; one cluster barrier. The two buffers
   // alternate, so a CTA writes a buffer again only after every reader of it
@@ -273,20 +345,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     cluster_sync();
   };
-  const auto block_total = [&](u64 v) {
-    v = warp_sum(v);
-    __syncthreads();
-    if (lane == 0) s.red[tid >> 5] = v;
-    __syncthreads();
-    u64 t = 0;
-    for (int i = 0; i < kWarps; ++i) t += s.red[i];
-    return t;
-  };
-  // Sums over the cluster's threads, and of its first value over the CTAs before this one.
-  u64 before_me = 0;
-  const auto cluster_sum = [&](const Sums& v) {
-    const u64 va = block_total(v.a), vb = block_total(v.b), vc = block_total(v.c);
-    exchange(va, vb, vc);
+  u64 before_me = 0;  // the first sum over the CTAs before this one
+  const auto gather_sums = [&]() {
     Sums t = {0, 0, 0};
     before_me = 0;
     for (int r = 0; r < C; ++r) {
@@ -298,30 +358,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     par ^= 1;
     return t;
   };
-  {
-    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
-    kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
-    valid32 = __reduce_add_sync(0xFFFFFFFFu, valid32);
+  const auto cluster_sum = [&](Sums v) {
+    v.a = warp_sum(v.a);
+    v.b = warp_sum(v.b);
+    __syncthreads();
     if (lane == 0) {
-      s.red[tid >> 5] = ((u64)kmax << 32) | kmin;
-      s.redd[0][tid >> 5] = (double)valid32;
+      s.red[0][wid] = v.a;
+      s.red[1][wid] = v.b;
     }
     __syncthreads();
-    cluster_wait();
-    u64 vmax = 0, vmin = 0xFFFFFFFFull, vn = 0;
-    for (int i = 0; i < kWarps; ++i) {
-      vmax = max(vmax, s.red[i] >> 32);
-      vmin = min(vmin, s.red[i] & 0xFFFFFFFFull);
-      vn += (u64)s.redd[0][i];
+    if (wid == 0) {
+      v.a = warp_sum(lane < kWarps ? s.red[0][lane] : 0ull);
+      v.b = warp_sum(lane < kWarps ? s.red[1][lane] : 0ull);
     }
-    exchange(vmax, vmin, vn);
+    exchange(v.a, v.b, 0ull);  // threads of warp 0 send
+    return gather_sums();
+  };
+  uint32_t kmax, kmin;
+  {
+    kmax = sample_key(fmx);
+    kmin = fmn < INFINITY ? sample_key(fmn) : (valid != 0u ? sample_key(INFINITY) : 0xFFFFFFFFu);
+    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
+    kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
+    valid = __reduce_add_sync(0xFFFFFFFFu, valid);
+    if (lane == 0) {
+      s.red[0][wid] = kmax;
+      s.red[1][wid] = kmin;
+      s.red[2][wid] = valid;
+    }
+    __syncthreads();
+    if (wid == 0) {
+      kmax = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? (uint32_t)s.red[0][lane] : 0u);
+      kmin = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? (uint32_t)s.red[1][lane] : 0xFFFFFFFFu);
+      valid = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? (uint32_t)s.red[2][lane] : 0u);
+    }
+    cluster_wait();
+    exchange(kmax, kmin, valid);
     kmax = 0u;
     kmin = 0xFFFFFFFFu;
-    valid32 = 0u;
+    valid = 0u;
     for (int r = 0; r < C; ++r) {
       kmax = max(kmax, (uint32_t)s.xch[par][r][0]);
       kmin = min(kmin, (uint32_t)s.xch[par][r][1]);
-      valid32 += (uint32_t)s.xch[par][r][2];
+      valid += (uint32_t)s.xch[par][r][2];
     }
     par ^= 1;
   }
@@ -336,12 +415,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   r.top = kmax;
   r.mxf = key_value(kmax);
   r.mx = (double)r.mxf;
-  r.c = greedy ? 0.0 : -369.329930467574631 / (double)T;  // 256 log2(e)
+  const double inv_t = 1.0 / (double)T;
+  r.c = greedy ? 0.0 : -369.329930467574631 * inv_t;  // 256 log2(e)
 
-  const auto finish = [&](int64_t token, uint32_t key, u64 total) {
+  const auto finish = [&](int64_t token, float x, u64 total) {
     p.tokens[b] = token;
     if (p.logprobs != nullptr) {
-      const double d = key == r.top ? 0.0 : ((double)key_value(key) - r.mx) / (double)T;
+      const double d = x == r.mxf ? 0.0 : ((double)x - r.mx) / (double)T;
       p.logprobs[b] = greedy ? 0.0f : (float)(d - log((double)total / kWeightOne));
     }
   };
@@ -354,41 +434,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (greedy) {  // the first token with the largest logit
     uint32_t first = 0xFFFFFFFFu;
     for (int i = tid; i < n; i += kThreads)
-      if (key_at(i) == r.top) first = min(first, (uint32_t)(i0 + i));
+      if (at(i) == r.mxf) first = min(first, (uint32_t)(i0 + i));
     first = __reduce_min_sync(0xFFFFFFFFu, first);
     __syncthreads();
-    if (lane == 0) s.red[tid >> 5] = first;
+    if (lane == 0) s.red[0][wid] = first;
     __syncthreads();
-    u64 mine = 0xFFFFFFFFull;
-    for (int i = 0; i < kWarps; ++i) mine = min(mine, s.red[i]);
-    exchange(mine, 0, 0);
+    if (wid == 0) first = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? (uint32_t)s.red[0][lane] : 0xFFFFFFFFu);
+    exchange(first, 0, 0);
     if (rank == 0 && tid == 0) {
-      u64 f = 0xFFFFFFFFull;
-      for (int c = 0; c < C; ++c) f = min(f, s.xch[par][c][0]);
-      finish((int64_t)f, r.top, 1ull << 40);
+      uint32_t f = 0xFFFFFFFFu;
+      for (int c = 0; c < C; ++c) f = min(f, (uint32_t)s.xch[par][c][0]);
+      finish((int64_t)f, r.mxf, 1ull << 40);
     }
     return;
   }
 
-  const double span = key_value(kmax) == INFINITY ? 0.0 : r.mx - (double)key_value(kmin);
-  const double reach = fmin(kTail * (double)T, span);  // the bins' range, in x
-  const bool tail_out = reach < span;                  // the last bin's weights are all zero
-  r.scale = span > 0.0 ? (float)((kBins - 1) / reach) : 1.0f;
-  const double delta = span > 0.0 ? reach / (double)T / (kBins - 1) : 0.0;  // exponent per bin
+  const float span = r.mxf < INFINITY ? r.mxf - key_value(kmin) : 0.0f;  // may round to infinity
+  const float reach = fminf((float)kTail * T, span);  // the bins' range, in x
+  const bool tail_out = reach < span;                 // the last bin's weights are all zero
+  r.scale = span > 0.0f ? (float)(kBins - 1) / reach : 1.0f;
   const int packed = p.per <= kPackMax ? 18 : 0;
 
-  // The kept tokens so far: key > cut and the first `ties` with key == cut.
-  uint32_t cut = 1u;
-  u64 ties = ~0ull;
-  bool cut_partial = false;
-  bool by_k = kset > 0 && (uint32_t)kset < valid32;
+  // The kept tokens so far: x > cut and the first `ties` with x == cut.
+  float cut = -INFINITY;
+  u64 ties = 0;
+  bool partial = true;  // more tokens than `ties` are at the cut
+  bool by_k = kset > 0 && (uint32_t)kset < valid;
 
-  // Histogram of the tokens with key >= cut into the leader's totals.
+  // Histogram of the tokens x > cut (all of those at the cut too, unless it is
+  // -inf) into the leader's totals.
   const auto histogram = [&]() {
+#pragma unroll 4
     for (int i = tid; i < n; i += kThreads) {
-      const uint32_t key = key_at(i);
-      if (key >= cut && key != 0u) {
-        const uint32_t v = bin16(key, r);
+      const float x = at(i);
+      if (x >= cut && x > -INFINITY) {
+        const uint32_t v = bin16(x, r);
         atomicAdd(&s.hist[v >> 4], packed != 0 ? (1u << 18) + (v & 15u) : 1u);
       }
     }
@@ -397,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       const uint32_t h = s.hist[i];
       if (h != 0u) {
         const uint32_t c = packed != 0 ? h >> 18 : h, o = packed != 0 ? h & 0x3FFFFu : 8u * h;
-        remote_add(lead_cnt + 4 * i, c);
-        if (o != 0u) remote_add(lead_off + 4 * i, o);
+        remote_red(lead_cnt + 4 * i, c);
+        if (o != 0u) remote_red(lead_off + 4 * i, o);
       }
     }
     cluster_sync();
@@ -407,24 +487,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const auto broadcast = [&]() {
     __syncthreads();
     if (rank == 0 && tid > 0 && tid < C) {
-      remote_store(remote_addr(&s.g_lo, tid), (uint32_t)s.g_lo);
-      remote_store(remote_addr(&s.g_hi, tid), (uint32_t)s.g_hi);
+      remote_store(remote_addr(&s.mode, tid), s.mode);
+      remote_store(remote_addr(&s.hi_key, tid), s.hi_key);
+      remote_store(remote_addr(&s.lo_key, tid), s.lo_key);
       remote_store(remote_addr(&s.cut, tid), s.cut);
+      remote_store(remote_addr(&s.cut_partial, tid), s.cut_partial);
       remote_store(remote_addr(&s.ties, tid), s.ties);
-      remote_store(remote_addr(&s.cut_partial, tid), (uint32_t)s.cut_partial);
     }
     cluster_sync();
   };
-  // Tokens of a CTA counted from the leader's bins: 4 per thread, in order.
-  constexpr int kPerThread = kBins / kThreads;
-  const auto collect = [&](int i, uint32_t key) {
-    const uint32_t at = remote_add(lead_n, 1u);
-    if (at < (uint32_t)kListMax) remote_store(lead_list + 8 * at, ((u64)key << 32) | (0xFFFFFFFFu - (uint32_t)(i0 + i)));
+  constexpr int kPerThread = kBins / kThreads;  // bins of a leader's thread, in order
+  const auto collect = [&](int i, float x) {
+    const uint32_t slot = atomicAdd(&s.local_n, 1u);
+    if (slot < (uint32_t)kListMax) s.local[slot] = ((u64)sample_key(x) << 32) | (0xFFFFFFFFu - (uint32_t)(i0 + i));
+  };
+  // This CTA's candidates to the leader's list; complete after a cluster barrier.
+  const auto flush = [&]() {
+    __syncthreads();
+    const uint32_t m = s.local_n < (uint32_t)kListMax ? s.local_n : (uint32_t)kListMax;
+    if (m != 0u) {
+      if (tid == 0) s.base = remote_add(lead_n, m);
+      __syncthreads();
+      const uint32_t to = s.base;
+      for (uint32_t i = tid; i < m && to + i < (uint32_t)kListMax; i += kThreads)
+        remote_store(lead_list + 8 * (to + i), s.local[i]);
+    }
   };
 
-  // From the leader's sorted list of `m` candidates that holds every kept token:
-  // apply top-k (keep), top-p (need: the sum to reach, 0: off) and min-p, and draw.
-  const auto draw_from_list = [&](int m, int keep, bool use_p, bool own_total, u64 row_total) {
+  // From the leader's list of candidates, which holds every kept token: apply
+  // top-k (keep), top-p (of row_total, or of the kept ones' sum) and min-p, and draw.
+  const auto draw_from_list = [&](int keep, bool use_p, bool own_total, u64 row_total) {
+    const int m = (int)s.list_n;
     block_sort(s.list, m, true);
     keep = keep < m ? keep : m;
     for (int i = tid; i < kListMax; i += kThreads)
@@ -447,13 +540,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     // Index order: sort index << 32 | place, then scan the weights in that order.
     for (int i = tid; i < m; i += kThreads) {
-      u64 w = s.wlist[i];
+      const u64 w = s.wlist[i];
       const uint32_t idx = 0xFFFFFFFFu - (uint32_t)s.list[i];
-      if (w < wmin) w = s.wlist[i] = 0ull;
-      s.list[i] = w == 0ull ? ~0ull : ((u64)idx << 32) | (uint32_t)i;
+      s.list[i] = w == 0ull || w < wmin ? ~0ull : ((u64)idx << 32) | (uint32_t)i;
     }
-    __syncthreads();
-    // Keys of the drawn token come back from its index.
     block_sort(s.list, m, false);
     u64 w[kE], sum = 0, total;
 #pragma unroll
@@ -469,18 +559,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     for (int j = 0; j < kE; ++j) {
       if (run <= target && target < run + w[j]) {
         const int64_t idx = (int64_t)(s.list[tid * kE + j] >> 32);
-        const char* at = static_cast<const char*>(p.logits) + (b * p.ld + idx) * (kBf16 ? 2 : 4);
+        const char* src = static_cast<const char*>(p.logits) + (b * p.ld + idx) * (kBf16 ? 2 : 4);
         finish(idx,
-               sample_key(kBf16 ? bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(at))
-                                : *reinterpret_cast<const float*>(at)),
+               clean(kBf16 ? bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(src))
+                           : *reinterpret_cast<const float*>(src)),
                total);
       }
       run += w[j];
     }
   };
-  // From the leader's list of `m` tokens of consecutive bins: the border after
+  // From the leader's list of the tokens of consecutive bins: the border after
   // the shortest run, largest first, of `need` tokens, or of weight `need`.
-  const auto settle = [&](int m, u64 need, bool by_weight) {
+  const auto settle = [&](u64 need, bool by_weight) {
+    const int m = (int)s.list_n;
     block_sort(s.list, m, true);
     constexpr int kE = kListMax / kThreads;
     u64 w[kE], sum = 0, all;
@@ -504,35 +595,43 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         s.cut = key;
         s.ties = (u64)(i - lo + 1);
-        s.cut_partial = i + 1 < m && (uint32_t)(s.list[i + 1] >> 32) == key;
+        s.cut_partial = i + 1 < m && (uint32_t)(s.list[i + 1] >> 32) == key ? 1u : 0u;
       }
       run += w[j];
     }
     __syncthreads();
+    if (tid == 0) s.list_n = 0u;
+  };
+  const auto take_cut = [&]() {
+    cut = key_value(s.cut);
+    ties = s.ties;
+    partial = s.cut_partial != 0u;
   };
   // The border without a list (more equal or near tokens than one holds):
   // bisection over the keys, a pass each. All CTAs take part and agree.
   const auto bisect = [&](u64 need, bool by_weight) {
-    const uint32_t cut0 = cut;
+    const float cut0 = cut;
     const u64 ties0 = ties;
-    const bool partial0 = cut_partial;
+    const bool partial0 = partial;
+    const uint32_t key0 = cut0 > -INFINITY ? sample_key(cut0) : 1u;
     const auto sums = [&](uint32_t from, u64& reached, u64& equal) {  // kept tokens >= from; those == from
       Sums v = {0, 0, 0};
       for (int i = tid; i < n; i += kThreads) {
-        const uint32_t key = key_at(i);
-        if (key < from || key == 0u || (partial0 && key == cut0)) continue;
-        v.a += by_weight ? key_weight(key, r, s.tab) : 1ull;
+        const float x = at(i);
+        const uint32_t key = sample_key(x);
+        if (key < from || key == 0u || (partial0 && x == cut0)) continue;
+        v.a += by_weight ? weight(x, r, s.tab) : 1ull;
         if (key == from) ++v.b;
       }
       v = cluster_sum(v);
-      if (partial0 && from <= cut0) {
-        v.a += ties0 * (by_weight ? key_weight(cut0, r, s.tab) : 1ull);
-        if (from == cut0) v.b += ties0;
+      if (partial0 && from <= key0) {
+        v.a += ties0 * (by_weight ? weight(cut0, r, s.tab) : 1ull);
+        if (from == key0) v.b += ties0;
       }
       reached = v.a;
       equal = v.b;
     };
-    uint32_t lo = cut0, hi = r.top;  // the largest key from which on the need is reached
+    uint32_t lo = key0, hi = r.top;  // the largest key from which on the need is reached
     u64 got, eq;
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo + 1u) / 2u;
@@ -545,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const u64 above = got - eq * w;
     u64 want = w > 0 ? (need - above + w - 1) / w : eq;
     want = want < 1 ? 1 : want;
-    cut = lo;
+    partial = want < eq || (partial0 && lo == key0);
+    cut = key_value(lo);
     ties = want;
-    cut_partial = want < eq || (partial0 && lo == cut0);
   };
 
   // ---- top-k
@@ -561,46 +660,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j) {
         if (run < (u64)kset && run + mine[j] >= (u64)kset) {
-          const int bin = tid * kPerThread + j;
-          // Everything down to this bin, or the bin alone, or (-1) neither fits a list.
-          s.g_hi = bin;
-          s.g_lo = run + mine[j] <= kListMax ? 0 : (mine[j] <= kListMax ? bin : -1);
-          if (s.g_lo < 0 && bin == kBins - 1 && tail_out) s.g_lo = -2;  // only zero weights are in question
+          const uint32_t bin = tid * kPerThread + j;
+          s.mode = run + mine[j] <= kListMax               ? kWhole
+                   : mine[j] <= kListMax                   ? kBorder
+                   : bin == kBins - 1 && tail_out          ? kZeros
+                                                           : kCrowd;
+          s.hi_key = s.mode == kWhole || bin == 0 ? 0xFFFFFFFFu : bin_key(bin, r);
+          s.lo_key = bin == kBins - 1 ? 1u : bin_key(bin + 1u, r);
           s.ties = (u64)kset - run;  // how many of the bin's tokens stay
         }
         run += mine[j];
       }
     }
     broadcast();
-    const int g_lo = s.g_lo, g_hi = s.g_hi;
-    const u64 in_bin = s.ties;
-    if (g_lo >= 0) {
+    const uint32_t mode = s.mode;
+    if (mode == kWhole || mode == kBorder) {
+      const uint32_t hk = s.hi_key, lk = s.lo_key;
+      const u64 in_bin = s.ties;
+#pragma unroll 4
       for (int i = tid; i < n; i += kThreads) {
-        const uint32_t key = key_at(i);
-        if (key == 0u) continue;
-        const int bin = (int)(bin16(key, r) >> 4);
-        if (bin >= g_lo && bin <= g_hi) collect(i, key);
+        const float x = at(i);
+        const uint32_t key = sample_key(x);
+        if (key >= lk && key < hk) collect(i, x);
       }
+      flush();
       cluster_sync();
-      // A list of one bin only settles top-k unless that bin is the first.
-      if (g_lo == 0) {
-        if (rank == 0) draw_from_list(s.list_n, kset, by_p, true, 0ull);
+      if (mode == kWhole) {
+        if (rank == 0) draw_from_list(kset, by_p, true, 0ull);
         return;
       }
-      if (rank == 0) {
-        settle(s.list_n, in_bin, false);
-        if (tid == 0) s.list_n = 0;
-      }
+      if (rank == 0) settle(in_bin, false);
       broadcast();
-      cut = s.cut;
-      ties = s.ties;
-      cut_partial = s.cut_partial != 0;
-    } else if (g_lo == -1) {
+      take_cut();
+    } else if (mode == kCrowd) {
       bisect((u64)kset, false);
     }
     if (by_p) {  // the histogram again, of what is left
       __syncthreads();
       for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
+      if (tid == 0) s.local_n = 0u;
       if (rank == 0)
         for (int i = tid; i < kBins; i += kThreads) s.total.cnt[i] = s.total.off[i] = 0u;
       cluster_sync();
@@ -612,8 +710,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // bank twice.
   const int own = ((n + kThreads - 1) / kThreads) | 1;
   const int t0 = own * tid < n ? own * tid : n, t1 = t0 + own < n ? t0 + own : n;
-  u64 sure = 0;    // weight of the thread's tokens that are kept whatever the border
-  int g_lo = 0;    // first bin that `sure` does not cover
+  u64 sure = 0;           // weight of the thread's tokens that are kept whatever the border
+  float sure_from = __uint_as_float(0x7FC00000u);  // those x >= it (none, for a NaN)
 
   // ---- top-p
   if (by_p) {
@@ -622,183 +720,185 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // Bounds of every bin's weight: a token f bins past the bin's start
       // weighs e^(-delta f), between 1 - delta f and the chord; f is known to half
       // a sixteenth (and the rounding of the bin position, below 0.01 bins), or
-      // not at all without the sixteenths.
-      double lo[kPerThread], hi[kPerThread], slo = 0.0, shi = 0.0;
-      const double fe = packed != 0 ? 1.0 / 32.0 + 0.01 : 0.51;
-      const double shrink = 1.0 - exp(-delta);
+      // not at all without the sixteenths. In fp32, whose errors over 2048
+      // additions stay below the 1e-3 that the borders are widened by.
+      // Exponent per bin (no bins to speak of where all tokens are equal or T is infinite).
+      const float delta = span > 0.0f && inv_t > 0.0 ? (float)(inv_t / (double)r.scale) : 0.0f;
+      const float fe = packed != 0 ? 1.0f / 32.0f + 0.01f : 0.51f;
+      const float shrink = delta < 1.0f ? delta * (1.0f - delta * (0.5f - delta * (1.0f / 6.0f))) : 1.0f;
+      const float step = expf(-delta);
+      float e = expf(-delta * (float)(tid * kPerThread));
+      float lo[kPerThread], hi[kPerThread], slo = 0.f, shi = 0.f;
+      u64 mine[kPerThread], cnt = 0, all;
+      const uint32_t cut_bin = cut > -INFINITY && partial ? bin16(cut, r) >> 4 : 0xFFFFFFFFu;
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j) {
         const int bin = tid * kPerThread + j;
-        const double c = s.total.cnt[bin], f = s.total.off[bin] * (1.0 / 16.0);
-        const double e = exp(-delta * bin);
-        lo[j] = c > 0.0 ? fmax(e * (c - delta * (f + c * fe)) - c / kWeightOne, 0.0) : 0.0;
-        hi[j] = c > 0.0 ? e * (c - shrink * (f - c * fe)) * (1.0 + delta * delta) + c / kWeightOne : 0.0;
-        if (bin == kBins - 1 || (cut_partial && bin == (int)(bin16(cut, r) >> 4))) lo[j] = 0.0;
-        if (bin == kBins - 1) hi[j] = c * e * (1.0 + delta) + c / kWeightOne;
+        cnt += mine[j] = s.total.cnt[bin];
+        const float c = (float)mine[j], f = (float)s.total.off[bin] * (1.0f / 16.0f);
+        const float slack = c * 1e-12f;  // the rounding to 2^-40
+        lo[j] = c > 0.f ? fmaxf(e * (c - delta * (f + c * fe)) - slack, 0.f) : 0.f;
+        hi[j] = c > 0.f ? e * (c - shrink * fmaxf(f - c * fe, 0.f)) * (1.0f + delta * delta + 0.1f * delta) + slack : 0.f;
+        if (bin == kBins - 1 || (uint32_t)bin == cut_bin) lo[j] = 0.f;
+        if (bin == kBins - 1) hi[j] = c * e * (1.0f + delta) + slack;
         slo += lo[j];
         shi += hi[j];
+        e *= step;
       }
-      // Prefixes of both.
-      const int warp = tid >> 5;
-      double plo = slo, phi = shi;
+      float plo = slo, phi = shi;  // prefixes of both
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const double a = __shfl_up_sync(0xFFFFFFFFu, plo, d), c = __shfl_up_sync(0xFFFFFFFFu, phi, d);
+        const float x = __shfl_up_sync(0xFFFFFFFFu, plo, d), y = __shfl_up_sync(0xFFFFFFFFu, phi, d);
         if (lane >= d) {
-          plo += a;
-          phi += c;
+          plo += x;
+          phi += y;
         }
       }
       if (lane == 31) {
-        s.redd[0][warp] = plo;
-        s.redd[1][warp] = phi;
+        s.redf[0][wid] = plo;
+        s.redf[1][wid] = phi;
       }
-      if (tid == 0) {
-        s.g_lo = kBins - 1;
-        s.g_hi = kBins - 1;
-      }
-      __syncthreads();
-      double tlo = 0.0, thi = 0.0;
+      if (tid == 0) s.bin_lo = s.bin_hi = kBins - 1;
+      u64 run = block_scan(cnt, s, all);  // its barriers order the lines around it
+      float tlo = 0.f, thi = 0.f;
       plo -= slo;
       phi -= shi;
       for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) {
-          plo += s.redd[0][i];
-          phi += s.redd[1][i];
+        if (i < wid) {
+          plo += s.redf[0][i];
+          phi += s.redf[1][i];
         }
-        tlo += s.redd[0][i];
-        thi += s.redd[1][i];
+        tlo += s.redf[0][i];
+        thi += s.redf[1][i];
       }
-      const double want_lo = pp * tlo * (1.0 - 1e-9), want_hi = pp * thi * (1.0 + 1e-9);
+      const float want_lo = (float)pp * tlo * (1.0f - 1e-5f), want_hi = (float)pp * thi * (1.0f + 1e-5f);
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j) {
         const int bin = tid * kPerThread + j;
-        if (phi + hi[j] >= want_lo) atomicMin(&s.g_lo, bin);
-        if (plo + lo[j] >= want_hi) atomicMin(&s.g_hi, bin);
+        if ((phi + hi[j]) * (1.0f + 1e-3f * delta + 1e-5f) >= want_lo) atomicMin(&s.bin_lo, bin);
+        if ((plo + lo[j]) * (1.0f - 1e-3f * delta - 1e-5f) >= want_hi) atomicMin(&s.bin_hi, bin);
         plo += lo[j];
         phi += hi[j];
       }
       __syncthreads();
-      u64 mine[kPerThread], sum = 0, all;
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j) sum += mine[j] = s.total.cnt[tid * kPerThread + j];
-      u64 run = block_scan(sum, s, all);
-      const int blo = s.g_lo, bhi = s.g_hi;
-      u64 upto = 0, inside = 0;  // tokens in bins 0..bhi and blo..bhi
+      const int blo = s.bin_lo, bhi = s.bin_hi;
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j) {
         const int bin = tid * kPerThread + j;
-        if (bin <= bhi) upto += mine[j];
-        if (bin >= blo && bin <= bhi) inside += mine[j];
+        if (bin == blo) s.red[1][0] = run;            // tokens before the candidates' bins
+        if (bin == bhi) s.red[1][1] = run + mine[j];  // and through them
+        run += mine[j];
       }
-      (void)run;
-      u64 dummy;
-      block_scan(upto, s, dummy);
-      upto = dummy;
-      block_scan(inside, s, dummy);
-      inside = dummy;
       __syncthreads();
       if (tid == 0) {
-        if (upto <= kListMax) s.g_lo = 0;
-        else if (inside > kListMax) s.g_lo = -1;
-        s.cut = cut;
-        s.ties = ties;
-        s.cut_partial = cut_partial ? 1 : 0;
+        const u64 before = s.red[1][0], through = s.red[1][1];
+        s.mode = through <= kListMax ? kWhole : (through - before <= kListMax ? kBorder : kCrowd);
+        s.hi_key = s.mode == kWhole || blo == 0 ? 0xFFFFFFFFu : bin_key(blo, r);
+        s.cut = 0u;
+        s.cut_partial = 0u;
+        s.ties = 0u;
       }
+      if (tid == 32) s.lo_key = bhi == kBins - 1 ? 1u : bin_key(bhi + 1, r);
     }
     broadcast();
-    g_lo = s.g_lo;
-    const int g_hi = s.g_hi;
+    const uint32_t mode = s.mode, hk = s.hi_key, lk = s.lo_key;
+    // Candidates: lo_x <= x < hi_x; kept whatever the border: x >= hi_x (never, for a NaN).
+    const float hi_x = hk == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(hk);
+    const float lo_x = lk <= 0x007FFFFFu ? -INFINITY : key_value(lk);
     // One pass with an exponential per token: the sum of all kept tokens, of
-    // those before bin g_lo, and the candidates between.
+    // those above the candidates, and the candidates. A sum of weight bits holds
+    // kMagicBits once per token, taken off at the end; the largest logit
+    // and those beside an infinite one take no exponential.
     Sums v = {0, 0, 0};
+    const bool inf = r.mxf == INFINITY;
+    const bool list = mode != kCrowd;
+#pragma unroll 4
     for (int i = t0; i < t1; ++i) {
-      const uint32_t key = key_at(i);
-      if (key < cut || key == 0u || (cut_partial && key == cut)) {
-        if (key == cut && key != 0u && g_lo >= 0) {  // a tie of top-k's border: counted by its rank, below
-          const int bin = (int)(bin16(key, r) >> 4);
-          if (bin >= g_lo && bin <= g_hi) collect(i, key);
+      const float x = at(i);
+      const bool tie = partial && x == cut;  // a tie of top-k's border: counted by its rank
+      if (x >= cut && x > -INFINITY) {
+        u64 w = inf ? kMagicBits : weight_bits(x, r, s.tab);
+        if (x == r.mxf) w = kMagicBits + (1ull << 40);
+        w -= kMagicBits;
+        if (!tie) v.a += w;
+        if (x >= hi_x) {
+          v.b += w;
+          if (w >= wmin) sure += w;
+        } else if (list && x >= lo_x) {
+          collect(i, x);
         }
-        continue;
-      }
-      const u64 w = key_weight(key, r, s.tab);
-      v.a += w;
-      if (g_lo < 0) continue;
-      const int bin = (int)(bin16(key, r) >> 4);
-      if (bin < g_lo) {
-        v.b += w;
-        if (w >= wmin) sure += w;
-      } else if (bin <= g_hi) {
-        collect(i, key);
       }
     }
+    if (list) flush();
     v = cluster_sum(v);  // its barrier also completes the list
-    const u64 total = v.a + (cut_partial ? ties * key_weight(cut, r, s.tab) : 0ull);
+    const u64 total = v.a + (partial && ties > 0 ? ties * weight(cut, r, s.tab) : 0ull);
     const double want = ceil(pp * (double)total);
     const u64 need = want > 1.0 ? (u64)want : 1ull;
-    if (g_lo == 0) {
+    if (mode == kWhole) {
       // All that can stay is in the list; top-k's border cuts it at kset tokens.
-      if (rank == 0) draw_from_list(s.list_n, by_k ? kset : kListMax, true, false, total);
+      if (rank == 0) draw_from_list(by_k ? kset : kListMax, true, false, total);
       return;
     }
-    if (g_lo > 0) {
-      if (rank == 0) settle(s.list_n, need - v.b, true);
+    if (mode == kBorder) {
+      if (rank == 0) settle(need - v.b, true);
       broadcast();
-      cut = s.cut;
-      ties = s.ties;
-      cut_partial = s.cut_partial != 0;
+      take_cut();
+      sure_from = hi_x;
     } else {
       bisect(need, true);
       sure = 0;
-      g_lo = 0;
     }
   }
 
   // ---- the draw, in index order
-  u64 tie = 0;  // rank of the thread's first token with key == cut
-  if (cut_partial) {
+  u64 tie = 0;  // rank of the thread's first token at the cut
+  const bool ranked = partial && ties > 0;
+  if (ranked) {
     u64 mine = 0, all;
-    for (int i = t0; i < t1; ++i) mine += key_at(i) == cut ? 1 : 0;
+    for (int i = t0; i < t1; ++i) mine += at(i) == cut ? 1 : 0;
     tie = block_scan(mine, s, all);
-    cluster_sum(Sums{mine, 0, 0});
+    exchange(all, 0, 0);
+    gather_sums();
     tie += before_me;
   }
-  const auto kept_weight = [&](uint32_t key, u64 rank_of_tie) {
-    if (key < cut || key == 0u || (cut_partial && key == cut && rank_of_tie >= ties)) return 0ull;
-    const u64 w = key_weight(key, r, s.tab);
+  const auto kept_weight = [&](float x, u64 rank_of_tie) {
+    if (!(x >= cut) || !(x > -INFINITY) || (partial && x == cut && rank_of_tie >= ties)) return 0ull;
+    const u64 w = weight(x, r, s.tab);
     return w >= wmin ? w : 0ull;
   };
   u64 sum = sure, tr = tie;
+#pragma unroll 4
   for (int i = t0; i < t1; ++i) {
-    const uint32_t key = key_at(i);
-    if (key < cut) continue;
-    if (g_lo > 0 && (int)(bin16(key, r) >> 4) < g_lo) continue;  // in `sure`
-    sum += kept_weight(key, tr);
-    if (key == cut) ++tr;
+    const float x = at(i);
+    if (x >= cut && !(x >= sure_from)) {
+      sum += kept_weight(x, tr);
+      if (x == cut) ++tr;
+    }
   }
   u64 mine_all;
   u64 run = block_scan(sum, s, mine_all);
-  const u64 total = cluster_sum(Sums{sum, 0, 0}).a, target = target_of(total);
+  exchange(mine_all, 0, 0);
+  const u64 total = gather_sums().a, target = target_of(total);
   run += before_me;
   // The warp whose lane's stretch holds the target walks that stretch together.
   const uint32_t hit = __ballot_sync(0xFFFFFFFFu, run <= target && target < run + sum);
   if (hit != 0u) {
     const int from = __ffs(hit) - 1;
     const int a0 = __shfl_sync(0xFFFFFFFFu, t0, from), a1 = __shfl_sync(0xFFFFFFFFu, t1, from);
-    u64 at = __shfl_sync(0xFFFFFFFFu, run, from), rk = __shfl_sync(0xFFFFFFFFu, tie, from);
+    u64 pos = __shfl_sync(0xFFFFFFFFu, run, from), rk = __shfl_sync(0xFFFFFFFFu, tie, from);
     for (int i = a0; i < a1; i += 32) {
-      const uint32_t key = i + lane < a1 ? key_at(i + lane) : 0u;
-      const uint32_t eq = __ballot_sync(0xFFFFFFFFu, key == cut && key != 0u);
-      const u64 w = kept_weight(key, rk + __popc(eq & ((1u << lane) - 1u)));
+      const float x = i + lane < a1 ? at(i + lane) : -INFINITY;
+      const uint32_t eq = __ballot_sync(0xFFFFFFFFu, x == cut && i + lane < a1);
+      const u64 w = kept_weight(x, rk + __popc(eq & ((1u << lane) - 1u)));
       u64 inc = w;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const u64 o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
         if (lane >= d) inc += o;
       }
-      const u64 end = at + inc;
-      if (end - w <= target && target < end) finish(i0 + i + lane, key, total);
-      at = __shfl_sync(0xFFFFFFFFu, end, 31);
+      const u64 end = pos + inc;
+      if (end - w <= target && target < end) finish(i0 + i + lane, x, total);
+      pos = __shfl_sync(0xFFFFFFFFu, end, 31);
       rk += __popc(eq);
     }
   }
@@ -808,8 +908,12 @@ template <bool kBf16, bool kResident>
 cudaError_t launch_sample_t(const SampleParams& p, int64_t B, int C, size_t smem, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   auto kern = sample_kernel<kBf16, kResident>;
-  const cudaError_t e = allow_smem(kern, kSampleSmemMax, allowed);
+  cudaError_t e = allow_smem(kern, kSampleSmemMax, allowed);
   if (e != cudaSuccess) return e;
+  if (C > 8) {  // more CTAs than every device has to support
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * C));
   cfg.blockDim = dim3(kThreads);
@@ -843,7 +947,7 @@ cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, i
   p.ld = ld;
   p.per = (int)((V + C - 1) / C);
   p.cluster = C;
-  const size_t need = sizeof(Smem) + 4 * (size_t)p.per;
+  const size_t need = sizeof(Smem) + 4 * (size_t)(p.per + 16);
   const bool resident = need <= kSampleSmemMax;
   const size_t smem = resident ? need : sizeof(Smem);
   // A launch takes fewer than 2^31 CTAs: long batches go in parts.
