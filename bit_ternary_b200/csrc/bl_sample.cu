@@ -66,6 +66,7 @@ struct alignas(16) Smem {
   alignas(16) double tab[256];           // 2^(40 + j / 256)
   alignas(16) u64 red[3][kWarps];
   alignas(16) float redf[2][kWarps];
+  alignas(16) uint32_t slice[2][kBins / 8];  // sums of this CTA's share of the bins
   int bin_lo, bin_hi;        // leader: bins of top-p's candidates
   alignas(16) u64 xch[2][kMaxCluster][4];  // what the CTAs of the cluster tell one another
   alignas(16) uint32_t list_n;           // leader
@@ -76,6 +77,7 @@ struct alignas(16) Smem {
   uint32_t cut;              // kept: key > cut, and the first `ties` with key == cut
   uint32_t cut_partial;      // more tokens than `ties` have that key
   alignas(8) u64 ties;
+  u64 need;                  // of the candidates (top-k)
 };
 // What the leader makes of a histogram.
 enum : uint32_t {
@@ -103,8 +105,10 @@ __device__ __forceinline__ uint32_t remote_add(uint32_t a, uint32_t v) {
   asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
   return old;
 }
-__device__ __forceinline__ void remote_red(uint32_t a, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+__device__ __forceinline__ uint32_t remote_load(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -121,8 +125,24 @@ struct Row {
   double mx;      // largest logit
   double c;       // -256 log2(e) / T
   uint32_t top;   // its key
-  float mxf, scale;  // bin position = (mxf - x) * scale
+  float mxf;
 };
+
+// 2^(40 + j / 256), by the exponential's series.
+struct alignas(16) Exp2Table {
+  double v[256];
+};
+constexpr Exp2Table make_exp2_table() {
+  Exp2Table t{};
+  for (int j = 0; j < 256; ++j) {
+    const double y = j * (0.693147180559945309417 / 256.0);
+    double sum = 0.0;
+    for (int i = 24; i > 0; --i) sum = (sum + 1.0) * y / i;
+    t.v[j] = (sum + 1.0) * kWeightOne;
+  }
+  return t;
+}
+__device__ const Exp2Table kExp2Table = make_exp2_table();
 
 // exp((x - max) / T) in units of 2^-40, by a table of 2^(j/256) and a cubic
 // (P. T. P. Tang, ACM TOMS 15(2), 1989): within 2^-42 relative before rounding.
@@ -152,22 +172,34 @@ __device__ __forceinline__ u64 key_weight(uint32_t key, const Row& r, const doub
   return weight(key_value(key), r, tab);
 }
 
-// Sixteenths of a bin from the largest logit; monotone in x.
-__device__ __forceinline__ uint32_t bin16(float x, const Row& r) {
-  if (x == r.mxf) return 0u;
-  const float pos = fminf((r.mxf - x) * r.scale, (float)(kBins - 1));
-  return (uint32_t)__float_as_int(fmaf(pos, 16.0f, 8388608.0f)) & 0x7FFFFFu;  // 2^23: rounds to an integer
+// kBins bins of equal width in x, from `origin` down.
+struct Bins {
+  float origin, scale;  // bin position = (origin - x) * scale
+};
+// Sixteenths of a bin from the origin; monotone in x.
+__device__ __forceinline__ uint32_t bin16(float x, const Bins& g) {
+  const float pos = fminf((g.origin - x) * g.scale, (float)(kBins - 1));
+  const uint32_t v = (uint32_t)__float_as_int(fmaf(pos, 16.0f, 8388608.0f)) & 0x7FFFFFu;  // 2^23: rounds
+  return x == g.origin ? 0u : v;  // infinities and a scale beyond fp32 included
 }
-// The smallest key whose token lies before bin `bin` (bin > 0).
-__device__ __forceinline__ uint32_t bin_key(uint32_t bin, const Row& r) {
-  uint32_t lo = 0u, hi = r.top;  // the largest logit lies in bin 0
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2u;
-    if (mid > 0x007FFFFFu && (bin16(key_value(mid), r) >> 4) < bin) hi = mid;  // smaller keys are -inf or NaN
-    else lo = mid + 1u;
+// The smallest key in (from, to] whose token lies before bin `bin`; `to` does.
+// By a warp, 32 probes at a time.
+__device__ __forceinline__ uint32_t bin_key(uint32_t bin, const Bins& g, uint32_t from, uint32_t to) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = from, hi = to;  // `lo` does not, or bounds the search
+  while (hi - lo > 1u) {
+    const uint32_t step = (hi - lo + 31u) / 32u;
+    const uint32_t probe = hi - lo <= step * (lane + 1u) ? hi : lo + step * (lane + 1u);
+    const bool before = (bin16(key_value(probe), g) >> 4) < bin;
+    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, before)) - 1;  // lane 31 probes hi
+    const uint32_t nhi = __shfl_sync(0xFFFFFFFFu, probe, first);
+    const uint32_t nlo = __shfl_sync(0xFFFFFFFFu, probe, first > 0 ? first - 1 : 0);
+    lo = first > 0 ? nlo : lo;
+    hi = nhi;
   }
-  return lo;
+  return hi;
 }
+constexpr uint32_t kNoKey = 0x007FFFFFu;  // the keys up to this one are -inf and NaN
 
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v) {
@@ -199,18 +231,43 @@ __device__ __forceinline__ u64 block_scan(u64 v, Smem& s, u64& all) {
   return before + inc - v;
 }
 
-// Sorts n entries of `a` (bitonic, padded to a power of two), largest first or
-// smallest first. A warp's 32 pairs of a stage lie in 64 entries of its own
-// while partners are at most 32 apart: those stages need no block barrier.
+// Sorts n <= kListMax entries of `a` (bitonic, padded to a power of two), largest
+// first or smallest first. Up to kThreads entries: one per thread in a register,
+// partners less than a warp apart by shuffles, the others through `a`. More: in
+// `a`, where a warp's 32 pairs of a stage lie in 64 entries of its own while
+// partners are at most 32 apart, so that those stages need no block barrier.
 __device__ __forceinline__ void block_sort(u64* a, int n, bool descending) {
+  const int tid = threadIdx.x;
   int p = 64;
   while (p < n) p <<= 1;
   __syncthreads();
-  for (int i = n + threadIdx.x; i < p; i += kThreads) a[i] = descending ? 0ull : ~0ull;
+  if (p <= kThreads) {
+    u64 x = tid < n ? a[tid] : (descending ? 0ull : ~0ull);
+    for (int k = 2; k <= p; k <<= 1) {
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        u64 y;
+        if (j >= 32) {
+          __syncthreads();
+          if (tid < p) a[tid] = x;
+          __syncthreads();
+          y = tid < p ? a[tid ^ j] : x;
+        } else {
+          y = __shfl_xor_sync(0xFFFFFFFFu, x, j);
+        }
+        const bool keep_small = ((tid & k) == 0) == ((tid & j) == 0);
+        x = (x > y) == (keep_small != descending) ? y : x;
+      }
+    }
+    __syncthreads();
+    if (tid < p) a[tid] = x;
+    __syncthreads();
+    return;
+  }
+  for (int i = n + tid; i < p; i += kThreads) a[i] = descending ? 0ull : ~0ull;
   __syncthreads();
   for (int k = 2; k <= p; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < (p >> 1); i += kThreads) {
+      for (int i = tid; i < (p >> 1); i += kThreads) {
         const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
         const u64 x = a[lo], y = a[hi];
         const bool up = ((lo & k) == 0) != descending;
@@ -251,6 +308,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // Another CTA's shared memory may be touched once it has begun: waited for
   // below, before the first exchange.
   cluster_arrive();
+
+  // ---- settings of the row, and what later passes start from
+  const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;
+  const int kset = p.how.top_k != nullptr ? p.how.top_k[b] : p.how.top_k_value;
+  const float pset = p.how.top_p != nullptr ? p.how.top_p[b] : p.how.top_p_value;
+  const float mset = p.how.min_p != nullptr ? p.how.min_p[b] : p.how.min_p_value;
+  const bool greedy = !(T > 0.0f);
+  const bool by_p = pset < 1.0f;  // false for NaN
+  const double pp = pset > 0.0f ? (double)pset : 0.0;
+  const u64 wmin = mset > 0.0f ? (u64)ceil((mset < 1.0f ? (double)mset : 1.0) * kWeightOne) : 0ull;
+
+  if (tid < 128) reinterpret_cast<double2*>(s.tab)[tid] = reinterpret_cast<const double2*>(kExp2Table.v)[tid];
+  for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
+  if (tid < kBins / 8) s.slice[0][tid] = s.slice[1][tid] = 0u;
+  if (tid == 0) s.list_n = s.local_n = 0u;
+  const uint32_t lead_list = remote_addr(s.list, 0), lead_n = remote_addr(&s.list_n, 0);
 
   // ---- the row, once: logits (NaN as -inf, -0 as 0), their extremes, how many are in
   const char* row = static_cast<const char*>(p.logits) + (b * p.ld + i0) * (kBf16 ? 2 : 4);
@@ -313,24 +386,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   } else {
     for (int i = tid; i < n; i += kThreads) note(load(i));
   }
-
-  // ---- settings of the row
-  const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;
-  const int kset = p.how.top_k != nullptr ? p.how.top_k[b] : p.how.top_k_value;
-  const float pset = p.how.top_p != nullptr ? p.how.top_p[b] : p.how.top_p_value;
-  const float mset = p.how.min_p != nullptr ? p.how.min_p[b] : p.how.min_p_value;
-  const bool greedy = !(T > 0.0f);
-  const bool by_p = pset < 1.0f;  // false for NaN
-  const double pp = pset > 0.0f ? (double)pset : 0.0;
-  const u64 wmin = mset > 0.0f ? (u64)ceil((mset < 1.0f ? (double)mset : 1.0) * kWeightOne) : 0ull;
-
-  for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
-  if (rank == 0)
-    for (int i = tid; i < kBins; i += kThreads) s.total.cnt[i] = s.total.off[i] = 0u;
-  if (tid == 0) s.list_n = s.local_n = 0u;
-  if (tid < 256) s.tab[tid] = exp2(40.0 + tid * (1.0 / 256.0));
-  const uint32_t lead_cnt = remote_addr(s.total.cnt, 0), lead_off = remote_addr(s.total.off, 0);
-  const uint32_t lead_list = remote_addr(s.list, 0), lead_n = remote_addr(&s.list_n, 0);
 
   // Three values of every CTA to all CTAs; one cluster barrier. The two buffers
   // alternate, so a CTA writes a buffer again only after every reader of it
@@ -452,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const float span = r.mxf < INFINITY ? r.mxf - key_value(kmin) : 0.0f;  // may round to infinity
   const float reach = fminf((float)kTail * T, span);  // the bins' range, in x
   const bool tail_out = reach < span;                 // the last bin's weights are all zero
-  r.scale = span > 0.0f ? (float)(kBins - 1) / reach : 1.0f;
+  const Bins whole{r.mxf, span > 0.0f ? (float)(kBins - 1) / reach : 1.0f};
   const int packed = p.per <= kPackMax ? 18 : 0;
 
   // The kept tokens so far: x > cut and the first `ties` with x == cut.
@@ -461,27 +516,53 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   bool partial = true;  // more tokens than `ties` are at the cut
   bool by_k = kset > 0 && (uint32_t)kset < valid;
 
-  // Histogram of the tokens x > cut (all of those at the cut too, unless it is
-  // -inf) into the leader's totals.
-  const auto histogram = [&]() {
+  // Histogram of the tokens with lo <= x < hi (no upper end for a NaN) into the
+  // leader's totals. Each CTA adds up its share of the bins over the cluster: an
+  // atomic per bin and CTA on the leader took four times as long.
+  const auto histogram = [&](const Bins& g, float lo, float hi) {
 #pragma unroll 4
     for (int i = tid; i < n; i += kThreads) {
       const float x = at(i);
-      if (x >= cut && x > -INFINITY) {
-        const uint32_t v = bin16(x, r);
+      if (x >= lo && x > -INFINITY && !(x >= hi)) {
+        const uint32_t v = bin16(x, g);
         atomicAdd(&s.hist[v >> 4], packed != 0 ? (1u << 18) + (v & 15u) : 1u);
       }
     }
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kThreads) {
-      const uint32_t h = s.hist[i];
-      if (h != 0u) {
-        const uint32_t c = packed != 0 ? h >> 18 : h, o = packed != 0 ? h & 0x3FFFFu : 8u * h;
-        remote_red(lead_cnt + 4 * i, c);
-        if (o != 0u) remote_red(lead_off + 4 * i, o);
+    cluster_sync();
+    const int share = kBins / C;  // bins of this CTA
+    const int groups = share < kThreads ? kThreads / share : 1, sources = C / groups;  // C = 8, 16: 2, 4 groups
+    for (int k = tid; k < share * groups; k += kThreads) {
+      const int bin = rank * share + k % share, from = k / share * sources;
+      uint32_t c = 0u, o = 0u;
+      for (int q = 0; q < sources; ++q) {
+        const uint32_t h = remote_load(remote_addr(&s.hist[bin], from + q));
+        c += packed != 0 ? h >> 18 : h;
+        o += packed != 0 ? h & 0x3FFFFu : 8u * h;
+      }
+      if (groups == 1) {
+        remote_store(remote_addr(&s.total.cnt[bin], 0), c);
+        remote_store(remote_addr(&s.total.off[bin], 0), o);
+      } else if (c != 0u) {
+        atomicAdd(&s.slice[0][k % share], c);
+        atomicAdd(&s.slice[1][k % share], o);
+      }
+    }
+    if (groups > 1) {
+      __syncthreads();
+      if (tid < share) {
+        remote_store(remote_addr(&s.total.cnt[rank * share + tid], 0), s.slice[0][tid]);
+        remote_store(remote_addr(&s.total.off[rank * share + tid], 0), s.slice[1][tid]);
+        s.slice[0][tid] = s.slice[1][tid] = 0u;
       }
     }
     cluster_sync();
+  };
+  // Ready for another histogram (its predecessor's readers are past a cluster barrier).
+  const auto clear_histogram = [&]() {
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
+    if (tid == 0) s.local_n = 0u;
+    __syncthreads();
   };
   // The leader's verdict to every CTA.
   const auto broadcast = [&]() {
@@ -493,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       remote_store(remote_addr(&s.cut, tid), s.cut);
       remote_store(remote_addr(&s.cut_partial, tid), s.cut_partial);
       remote_store(remote_addr(&s.ties, tid), s.ties);
+      remote_store(remote_addr(&s.need, tid), s.need);
     }
     cluster_sync();
   };
@@ -649,34 +731,194 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     ties = want;
   };
 
-  // ---- top-k
-  if (by_k) {
-    histogram();
-    if (rank == 0) {
-      u64 mine[kPerThread], sum = 0, all;
+  // Keys of the logits a bin's tokens have: [lo_key, hi_key), within [from, to).
+  const auto bin_range = [&](const Bins& g, uint32_t first, uint32_t last, uint32_t from, uint32_t to) {
+    // Two warps of the leader.
+    const uint32_t top = (to == 0xFFFFFFFFu ? r.top : to - 1u);  // lies in bin 0
+    if (wid == 0) {
+      const uint32_t k = first == 0u ? to : bin_key(first, g, from > kNoKey ? from - 1u : kNoKey, top);
+      if (lane == 0) s.hi_key = k;
+    } else if (wid == 1) {
+      const uint32_t k = last == kBins - 1 ? from : bin_key(last + 1u, g, from > kNoKey ? from - 1u : kNoKey, top);
+      if (lane == 0) s.lo_key = k;
+    }
+    __syncthreads();
+  };
+  // Leader: the bin of the need-th token of a histogram, and what to do about it.
+  const auto place_count = [&](const Bins& g, u64 need, bool may_whole, uint32_t from, uint32_t to) {
+    u64 mine[kPerThread], sum = 0, all;
 #pragma unroll
-      for (int j = 0; j < kPerThread; ++j) sum += mine[j] = s.total.cnt[tid * kPerThread + j];
-      u64 run = block_scan(sum, s, all);
+    for (int j = 0; j < kPerThread; ++j) sum += mine[j] = s.total.cnt[tid * kPerThread + j];
+    u64 run = block_scan(sum, s, all);
 #pragma unroll
-      for (int j = 0; j < kPerThread; ++j) {
-        if (run < (u64)kset && run + mine[j] >= (u64)kset) {
-          const uint32_t bin = tid * kPerThread + j;
-          s.mode = run + mine[j] <= kListMax               ? kWhole
-                   : mine[j] <= kListMax                   ? kBorder
-                   : bin == kBins - 1 && tail_out          ? kZeros
-                                                           : kCrowd;
-          s.hi_key = s.mode == kWhole || bin == 0 ? 0xFFFFFFFFu : bin_key(bin, r);
-          s.lo_key = bin == kBins - 1 ? 1u : bin_key(bin + 1u, r);
-          s.ties = (u64)kset - run;  // how many of the bin's tokens stay
-        }
-        run += mine[j];
+    for (int j = 0; j < kPerThread; ++j) {
+      if (run < need && run + mine[j] >= need) {
+        const int bin = tid * kPerThread + j;
+        s.mode = may_whole && run + mine[j] <= kListMax               ? kWhole
+                 : mine[j] <= kListMax                                ? kBorder
+                 : may_whole && bin == kBins - 1 && tail_out          ? kZeros
+                                                                      : kCrowd;
+        s.bin_hi = bin;
+        s.bin_lo = s.mode == kWhole ? 0 : bin;
+        s.need = need - run;  // how many of the bin's tokens stay
+        s.ties = mine[j];          // of how many
+      }
+      run += mine[j];
+    }
+    __syncthreads();
+    bin_range(g, s.bin_lo, s.bin_hi, from, to);
+  };
+  // Leader: the bins in which a running weight meets a target, by bounds of every
+  // bin's weight: a token f bins past the bin's start weighs e^(-delta f) of it,
+  // between 1 - delta f and the chord; f is known to half a sixteenth (and the
+  // rounding of the bin position, below 0.01 bins), or not at all without
+  // the sixteenths. `first` is the weight at the bins' origin. The target is
+  // share * total (target < 0) or a weight. In fp32, whose errors over 2048
+  // additions stay below the 1e-5 that the borders are widened by.
+  const auto place_weight = [&](const Bins& g, float first, float target, bool may_whole, uint32_t from, uint32_t to,
+                                bool open_end) {
+    // Exponent per bin (no bins to speak of where all tokens are equal or T is infinite).
+    const float delta = g.scale < INFINITY && inv_t > 0.0 ? fminf((float)(inv_t / (double)g.scale), 1.0f) : 0.0f;
+    const float fe = packed != 0 ? 1.0f / 32.0f + 0.01f : 0.51f;
+    const float shrink = delta * (1.0f - delta * (0.5f - delta * (1.0f / 6.0f)));
+    const float step = expf(-delta);
+    float e = first * expf(-delta * (float)(tid * kPerThread));
+    float lo[kPerThread], hi[kPerThread], slo = 0.f, shi = 0.f;
+    u64 mine[kPerThread], cnt = 0, all;
+    const uint32_t cut_bin = cut > -INFINITY && partial ? bin16(cut, g) >> 4 : 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int bin = tid * kPerThread + j;
+      cnt += mine[j] = s.total.cnt[bin];
+      const float c = (float)mine[j], f = (float)s.total.off[bin] * (1.0f / 16.0f);
+      const float slack = c * 1e-12f;  // the rounding to 2^-40
+      lo[j] = c > 0.f ? fmaxf(e * (c - delta * (f + c * fe)) - slack, 0.f) : 0.f;
+      hi[j] = c > 0.f ? e * (c - shrink * fmaxf(f - c * fe, 0.f)) * (1.0f + delta * delta + 0.1f * delta) + slack : 0.f;
+      if ((open_end && bin == kBins - 1) || (uint32_t)bin == cut_bin) lo[j] = 0.f;
+      slo += lo[j];
+      shi += hi[j];
+      e *= step;
+    }
+    float plo = slo, phi = shi;  // prefixes of both
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float x = __shfl_up_sync(0xFFFFFFFFu, plo, d), y = __shfl_up_sync(0xFFFFFFFFu, phi, d);
+      if (lane >= d) {
+        plo += x;
+        phi += y;
       }
     }
+    if (lane == 31) {
+      s.redf[0][wid] = plo;
+      s.redf[1][wid] = phi;
+    }
+    if (tid == 0) s.bin_lo = s.bin_hi = kBins - 1;
+    u64 run = block_scan(cnt, s, all);  // its barriers order the lines around it
+    float tlo = 0.f, thi = 0.f;
+    plo -= slo;
+    phi -= shi;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < wid) {
+        plo += s.redf[0][i];
+        phi += s.redf[1][i];
+      }
+      tlo += s.redf[0][i];
+      thi += s.redf[1][i];
+    }
+    const float want_lo = target < 0.f ? (float)pp * tlo : target, want_hi = target < 0.f ? (float)pp * thi : target;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int bin = tid * kPerThread + j;
+      if ((phi + hi[j]) * (1.0f + 1e-5f) >= want_lo * (1.0f - 1e-5f)) atomicMin(&s.bin_lo, bin);
+      if ((plo + lo[j]) * (1.0f - 1e-5f) >= want_hi * (1.0f + 1e-5f)) atomicMin(&s.bin_hi, bin);
+      plo += lo[j];
+      phi += hi[j];
+    }
+    __syncthreads();
+    const int blo = s.bin_lo, bhi = s.bin_hi;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int bin = tid * kPerThread + j;
+      if (bin == blo) s.red[1][0] = run;            // tokens before the candidates' bins
+      if (bin == bhi) s.red[1][1] = run + mine[j];  // and through them
+      run += mine[j];
+    }
+    __syncthreads();
+    const u64 before = s.red[1][0], through = s.red[1][1];
+    const uint32_t mode = may_whole && through <= kListMax ? kWhole : (through - before <= kListMax ? kBorder : kCrowd);
+    if (tid == 0) {
+      s.mode = mode;
+      s.ties = through - before;
+    }
+    bin_range(g, mode == kWhole ? 0u : (uint32_t)blo, (uint32_t)bhi, from, to);
+  };
+  // The border among the `count` tokens of keys [lk, hk), more than a list holds:
+  // finer bins over that range, until a list holds a bin's tokens or all have one
+  // value.
+  const auto zoom = [&](u64 need, bool by_weight, uint32_t lk, uint32_t hk, u64 count) {
+    for (int level = 0; level < 4; ++level) {
+      lk = max(max(lk, kmin), cut > -INFINITY ? sample_key(cut) : 0u);
+      if (by_weight) lk = max(lk, sample_key(r.mxf - (float)kTail * T));  // weights below are zero
+      const uint32_t last = hk == 0xFFFFFFFFu ? r.top : hk - 1u;
+      if (lk >= last) {  // ties
+        const u64 w = by_weight ? key_weight(last, r, s.tab) : 1ull;
+        if (w == 0ull) break;
+        cut = key_value(last);
+        ties = (need + w - 1) / w;
+        partial = ties < count;
+        return true;
+      }
+      const float lo_v = key_value(lk), hi_v = key_value(last);
+      const float width = hi_v - lo_v;
+      if (!(width > 0.0f && width < INFINITY)) break;
+      const Bins g{hi_v, (float)(kBins - 1) / width};
+      const float hi_x = hk == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(hk);
+      clear_histogram();
+      histogram(g, lo_v, hi_x);
+      if (rank == 0) {
+        if (by_weight)
+          place_weight(g, (float)((double)key_weight(last, r, s.tab) / kWeightOne), (float)((double)need / kWeightOne),
+                       false, lk, hk, false);
+        else
+          place_count(g, need, false, lk, hk);
+      }
+      broadcast();
+      const uint32_t mode = s.mode, nlk = s.lo_key, nhk = s.hi_key;
+      count = s.ties;
+      const u64 in_bin = s.need;
+      const bool list = mode == kBorder;
+      Sums v = {0, 0, 0};
+      for (int i = tid; i < n; i += kThreads) {
+        const float x = at(i);
+        const uint32_t key = sample_key(x);
+        if (key < nlk || key >= hk) continue;
+        if (key >= nhk) v.b += by_weight ? weight(x, r, s.tab) : 0ull;
+        else if (list) collect(i, x);
+      }
+      if (list) flush();
+      v = cluster_sum(v);
+      need = by_weight ? need - v.b : in_bin;
+      if (list) {
+        if (rank == 0) settle(need, by_weight);
+        broadcast();
+        take_cut();
+        return true;
+      }
+      if (nlk == lk && nhk == hk) break;
+      lk = nlk;
+      hk = nhk;
+    }
+    return false;
+  };
+
+  // ---- top-k
+  if (by_k) {
+    histogram(whole, -INFINITY, __uint_as_float(0x7FC00000u));
+    if (rank == 0) place_count(whole, (u64)kset, true, 1u, 0xFFFFFFFFu);
     broadcast();
-    const uint32_t mode = s.mode;
+    const uint32_t mode = s.mode, hk = s.hi_key, lk = s.lo_key;
+    const u64 in_bin = s.need, count = s.ties;
     if (mode == kWhole || mode == kBorder) {
-      const uint32_t hk = s.hi_key, lk = s.lo_key;
-      const u64 in_bin = s.ties;
 #pragma unroll 4
       for (int i = tid; i < n; i += kThreads) {
         const float x = at(i);
@@ -692,17 +934,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (rank == 0) settle(in_bin, false);
       broadcast();
       take_cut();
-    } else if (mode == kCrowd) {
+    } else if (mode == kCrowd && !zoom(in_bin, false, lk, hk, count)) {
       bisect((u64)kset, false);
     }
-    if (by_p) {  // the histogram again, of what is left
-      __syncthreads();
-      for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
-      if (tid == 0) s.local_n = 0u;
-      if (rank == 0)
-        for (int i = tid; i < kBins; i += kThreads) s.total.cnt[i] = s.total.off[i] = 0u;
-      cluster_sync();
-    }
+    if (by_p) clear_histogram();  // again, of what is left
   }
 
   // Thread t owns tokens [t * own, (t + 1) * own) of the CTA's stretch from here
@@ -715,96 +950,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
   // ---- top-p
   if (by_p) {
-    histogram();
-    if (rank == 0) {
-      // Bounds of every bin's weight: a token f bins past the bin's start
-      // weighs e^(-delta f), between 1 - delta f and the chord; f is known to half
-      // a sixteenth (and the rounding of the bin position, below 0.01 bins), or
-      // not at all without the sixteenths. In fp32, whose errors over 2048
-      // additions stay below the 1e-3 that the borders are widened by.
-      // Exponent per bin (no bins to speak of where all tokens are equal or T is infinite).
-      const float delta = span > 0.0f && inv_t > 0.0 ? (float)(inv_t / (double)r.scale) : 0.0f;
-      const float fe = packed != 0 ? 1.0f / 32.0f + 0.01f : 0.51f;
-      const float shrink = delta < 1.0f ? delta * (1.0f - delta * (0.5f - delta * (1.0f / 6.0f))) : 1.0f;
-      const float step = expf(-delta);
-      float e = expf(-delta * (float)(tid * kPerThread));
-      float lo[kPerThread], hi[kPerThread], slo = 0.f, shi = 0.f;
-      u64 mine[kPerThread], cnt = 0, all;
-      const uint32_t cut_bin = cut > -INFINITY && partial ? bin16(cut, r) >> 4 : 0xFFFFFFFFu;
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j) {
-        const int bin = tid * kPerThread + j;
-        cnt += mine[j] = s.total.cnt[bin];
-        const float c = (float)mine[j], f = (float)s.total.off[bin] * (1.0f / 16.0f);
-        const float slack = c * 1e-12f;  // the rounding to 2^-40
-        lo[j] = c > 0.f ? fmaxf(e * (c - delta * (f + c * fe)) - slack, 0.f) : 0.f;
-        hi[j] = c > 0.f ? e * (c - shrink * fmaxf(f - c * fe, 0.f)) * (1.0f + delta * delta + 0.1f * delta) + slack : 0.f;
-        if (bin == kBins - 1 || (uint32_t)bin == cut_bin) lo[j] = 0.f;
-        if (bin == kBins - 1) hi[j] = c * e * (1.0f + delta) + slack;
-        slo += lo[j];
-        shi += hi[j];
-        e *= step;
-      }
-      float plo = slo, phi = shi;  // prefixes of both
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float x = __shfl_up_sync(0xFFFFFFFFu, plo, d), y = __shfl_up_sync(0xFFFFFFFFu, phi, d);
-        if (lane >= d) {
-          plo += x;
-          phi += y;
-        }
-      }
-      if (lane == 31) {
-        s.redf[0][wid] = plo;
-        s.redf[1][wid] = phi;
-      }
-      if (tid == 0) s.bin_lo = s.bin_hi = kBins - 1;
-      u64 run = block_scan(cnt, s, all);  // its barriers order the lines around it
-      float tlo = 0.f, thi = 0.f;
-      plo -= slo;
-      phi -= shi;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < wid) {
-          plo += s.redf[0][i];
-          phi += s.redf[1][i];
-        }
-        tlo += s.redf[0][i];
-        thi += s.redf[1][i];
-      }
-      const float want_lo = (float)pp * tlo * (1.0f - 1e-5f), want_hi = (float)pp * thi * (1.0f + 1e-5f);
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j) {
-        const int bin = tid * kPerThread + j;
-        if ((phi + hi[j]) * (1.0f + 1e-3f * delta + 1e-5f) >= want_lo) atomicMin(&s.bin_lo, bin);
-        if ((plo + lo[j]) * (1.0f - 1e-3f * delta - 1e-5f) >= want_hi) atomicMin(&s.bin_hi, bin);
-        plo += lo[j];
-        phi += hi[j];
-      }
-      __syncthreads();
-      const int blo = s.bin_lo, bhi = s.bin_hi;
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j) {
-        const int bin = tid * kPerThread + j;
-        if (bin == blo) s.red[1][0] = run;            // tokens before the candidates' bins
-        if (bin == bhi) s.red[1][1] = run + mine[j];  // and through them
-        run += mine[j];
-      }
-      __syncthreads();
-      if (tid == 0) {
-        const u64 before = s.red[1][0], through = s.red[1][1];
-        s.mode = through <= kListMax ? kWhole : (through - before <= kListMax ? kBorder : kCrowd);
-        s.hi_key = s.mode == kWhole || blo == 0 ? 0xFFFFFFFFu : bin_key(blo, r);
-        s.cut = 0u;
-        s.cut_partial = 0u;
-        s.ties = 0u;
-      }
-      if (tid == 32) s.lo_key = bhi == kBins - 1 ? 1u : bin_key(bhi + 1, r);
-    }
+    histogram(whole, cut, __uint_as_float(0x7FC00000u));
+    if (rank == 0) place_weight(whole, 1.0f, -1.0f, true, 1u, 0xFFFFFFFFu, true);
     broadcast();
     const uint32_t mode = s.mode, hk = s.hi_key, lk = s.lo_key;
+    const u64 count = s.ties;
     // Candidates: lo_x <= x < hi_x; kept whatever the border: x >= hi_x (never, for a NaN).
     const float hi_x = hk == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(hk);
-    const float lo_x = lk <= 0x007FFFFFu ? -INFINITY : key_value(lk);
+    const float lo_x = lk <= kNoKey ? -INFINITY : key_value(lk);
     // One pass with an exponential per token: the sum of all kept tokens, of
     // those above the candidates, and the candidates. A sum of weight bits holds
     // kMagicBits once per token, taken off at the end; the largest logit
@@ -815,19 +968,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll 4
     for (int i = t0; i < t1; ++i) {
       const float x = at(i);
-      const bool tie = partial && x == cut;  // a tie of top-k's border: counted by its rank
-      if (x >= cut && x > -INFINITY) {
-        u64 w = inf ? kMagicBits : weight_bits(x, r, s.tab);
-        if (x == r.mxf) w = kMagicBits + (1ull << 40);
-        w -= kMagicBits;
-        if (!tie) v.a += w;
-        if (x >= hi_x) {
-          v.b += w;
-          if (w >= wmin) sure += w;
-        } else if (list && x >= lo_x) {
-          collect(i, x);
-        }
-      }
+      u64 w = weight_bits(x, r, s.tab) - kMagicBits;  // of -inf: zero
+      w = inf ? 0ull : w;
+      w = x == r.mxf ? 1ull << 40 : w;
+      w = x >= cut ? w : 0ull;
+      const bool above = x >= hi_x;
+      v.a += partial && x == cut ? 0ull : w;  // a tie of top-k's border is counted by its rank
+      v.b += above ? w : 0ull;
+      sure += above && w >= wmin ? w : 0ull;
+      if (list && !above && x >= lo_x && x >= cut && x > -INFINITY) collect(i, x);
     }
     if (list) flush();
     v = cluster_sum(v);  // its barrier also completes the list
@@ -843,6 +992,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (rank == 0) settle(need - v.b, true);
       broadcast();
       take_cut();
+      sure_from = hi_x;
+    } else if (zoom(need - v.b, true, lk, hk, count)) {
       sure_from = hi_x;
     } else {
       bisect(need, true);
