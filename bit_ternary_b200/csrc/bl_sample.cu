@@ -8,9 +8,9 @@
 // A cluster of 1 to 16 CTAs owns a row: each CTA reads its stretch once into
 // shared memory, and every later pass runs there. The thresholds of top-k and
 // top-p come from one histogram of 2048 bins, linear in x, of one 32-bit atomic
-// per token: a count and the sum of the tokens' sixteenths of a bin. Counts place
-// the k-th token in a bin exactly; the sixteenths bound every bin's weight to
-// about 0.1%, which places the border of top-p within a bin or two without an
+// per token: a count and the sum of the tokens' places in the bin. Counts place
+// the k-th token in a bin exactly; the places bound every bin's weight to
+// about 0.05%, which places the border of top-p within a bin or two without an
 // exponential. The tokens of those bins (some hundreds) are sorted and settle
 // the border exactly. Top-p then needs one exponential per token for the exact
 // sum, a draw without filters likewise, top-k none beyond the kept tokens.
@@ -22,12 +22,12 @@ namespace bl {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 32;
 constexpr int kBins = 2048;          // the last one holds what lies past the range
-constexpr int kListMax = 2048;       // tokens that a list of candidates holds
+constexpr int kListMax = 1024;       // tokens that a list of candidates holds
+constexpr int kWholeMax = 512;       // up to this many the draw itself runs from the list (a sort in registers)
 constexpr int kMaxCluster = 16;
-constexpr int kPackMax = 16383;      // tokens per CTA whose count and sixteenths fit 14 + 18 bits
+constexpr int kPackMax = 16383;      // tokens per CTA whose count and places fit 14 + 18 bits
 constexpr size_t kSampleSmemMax = 225 * 1024;
 constexpr double kWeightOne = 1099511627776.0;  // 2^40
 constexpr double kTail = 29.0;       // exp(-29) * 2^40 rounds to zero
@@ -47,46 +47,30 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // Shared memory of a CTA; the logits follow it. Every member starts on a 16-byte
-// boundary. Two regions serve twice: the
-// leader's totals hold the candidates once a border's bins are known, its
-// histogram their weights.
+// boundary.
 struct alignas(16) Smem {
+  uint32_t cnt[kBins], off[kBins];  // the row's histogram: counts and sums of places
+  alignas(16) u64 list[kListMax];   // the row's candidates: key << 32 | ~index
   union {
-    struct {
-      uint32_t cnt[kBins];
-      uint32_t off[kBins];
-    } total;                 // leader: counts and sixteenths of the row
-    u64 list[kListMax];      // leader: key << 32 | ~index
-  };
-  union {
-    uint32_t hist[kBins];    // this CTA: count << 18 | sixteenths, or counts
-    u64 local[kListMax];     // this CTA's candidates, on their way to the leader
-    u64 wlist[kListMax];     // leader: weights of the list
+    uint32_t hist[kBins];    // this CTA's histogram: counts above sums of places
+    u64 local[kListMax];     // this CTA's candidates
+    u64 wlist[kListMax];     // weights of the list
   };
   alignas(16) double tab[256];           // 2^(40 + j / 256)
-  alignas(16) u64 red[3][kWarps];
-  alignas(16) float redf[2][kWarps];
-  alignas(16) uint32_t slice[2][kBins / 8];  // sums of this CTA's share of the bins
-  int bin_lo, bin_hi;        // leader: bins of top-p's candidates
+  alignas(16) u64 red[3][kMaxWarps];
+  alignas(16) float redf[2][kMaxWarps];
   alignas(16) u64 xch[2][kMaxCluster][4];  // what the CTAs of the cluster tell one another
-  alignas(16) uint32_t list_n;           // leader
-  uint32_t local_n, base;    // this CTA's candidates, and where they go in the list
-  // Broadcast by the leader.
+  alignas(16) uint32_t slice[2][kBins / 8];  // sums of this CTA's share of the bins
+  alignas(16) uint32_t list_n;           // of the first CTA: places given out in the lists
+  uint32_t local_n, base;    // this CTA's candidates, and their place in the lists
+  int bin_lo, bin_hi;        // bins of the candidates
   uint32_t mode;
-  uint32_t hi_key, lo_key;   // candidates: lo_key <= key < hi_key
+  uint32_t lo_key, hi_key;   // their keys: lo_key <= key < hi_key
   uint32_t cut;              // kept: key > cut, and the first `ties` with key == cut
   uint32_t cut_partial;      // more tokens than `ties` have that key
-  alignas(8) u64 ties;
-  u64 need;                  // of the candidates (top-k)
+  alignas(16) u64 ties, need, count;
 };
-// What the leader makes of a histogram.
-enum : uint32_t {
-  kWhole,   // the candidates are all that can stay: draw from the list
-  kBorder,  // the candidates hold the border
-  kCrowd,   // more of them than a list holds
-  kZeros,   // only tokens of weight zero are in question
-};
-static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, xch) % 16 == 0, "alignment");
+static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, xch) % 16 == 0 && offsetof(Smem, ties) % 16 == 0, "alignment");
 
 // Shared memory of another CTA of the cluster, by its address there.
 __device__ __forceinline__ uint32_t remote_addr(const void* mine, int rank) {
@@ -119,6 +103,14 @@ __device__ __forceinline__ void cluster_sync() {
 }
 struct Sums {
   u64 a, b, c;
+};
+
+// What follows from a histogram.
+enum : uint32_t {
+  kWhole,   // the candidates are all that can stay: draw from the list
+  kBorder,  // the candidates hold the border
+  kCrowd,   // more of them than a list holds
+  kZeros,   // only tokens of weight zero are in question
 };
 
 struct Row {
@@ -176,10 +168,10 @@ __device__ __forceinline__ u64 key_weight(uint32_t key, const Row& r, const doub
 struct Bins {
   float origin, scale;  // bin position = (origin - x) * scale
 };
-// Sixteenths of a bin from the origin; monotone in x.
-__device__ __forceinline__ uint32_t bin16(float x, const Bins& g) {
+// 64ths of a bin from the origin; monotone in x.
+__device__ __forceinline__ uint32_t bin64(float x, const Bins& g) {
   const float pos = fminf((g.origin - x) * g.scale, (float)(kBins - 1));
-  const uint32_t v = (uint32_t)__float_as_int(fmaf(pos, 16.0f, 8388608.0f)) & 0x7FFFFFu;  // 2^23: rounds
+  const uint32_t v = (uint32_t)__float_as_int(fmaf(pos, 64.0f, 8388608.0f)) & 0x7FFFFFu;  // 2^23: rounds
   return x == g.origin ? 0u : v;  // infinities and a scale beyond fp32 included
 }
 // The smallest key in (from, to] whose token lies before bin `bin`; `to` does.
@@ -190,7 +182,7 @@ __device__ __forceinline__ uint32_t bin_key(uint32_t bin, const Bins& g, uint32_
   while (hi - lo > 1u) {
     const uint32_t step = (hi - lo + 31u) / 32u;
     const uint32_t probe = hi - lo <= step * (lane + 1u) ? hi : lo + step * (lane + 1u);
-    const bool before = (bin16(key_value(probe), g) >> 4) < bin;
+    const bool before = (bin64(key_value(probe), g) >> 6) < bin;
     const int first = __ffs(__ballot_sync(0xFFFFFFFFu, before)) - 1;  // lane 31 probes hi
     const uint32_t nhi = __shfl_sync(0xFFFFFFFFu, probe, first);
     const uint32_t nlo = __shfl_sync(0xFFFFFFFFu, probe, first > 0 ? first - 1 : 0);
@@ -209,7 +201,9 @@ __device__ __forceinline__ T warp_sum(T v) {
 }
 
 // Exclusive prefix over the block; the block's sum in `all`.
+template <int kThreads>
 __device__ __forceinline__ u64 block_scan(u64 v, Smem& s, u64& all) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   u64 inc = v;
 #pragma unroll
@@ -220,15 +214,15 @@ __device__ __forceinline__ u64 block_scan(u64 v, Smem& s, u64& all) {
   __syncthreads();
   if (lane == 31) s.red[0][warp] = inc;
   __syncthreads();
-  u64 before = 0, t = 0;
+  u64 w = lane < kWarps ? s.red[0][lane] : 0ull;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const u64 x = s.red[0][i];
-    if (i < warp) before += x;
-    t += x;
+  for (int d = 1; d < kWarps; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+    if (lane >= d) w += o;
   }
-  all = t;
-  return before + inc - v;
+  all = __shfl_sync(0xFFFFFFFFu, w, kWarps - 1);
+  const u64 before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0ull) + inc - v;
 }
 
 // Sorts n <= kListMax entries of `a` (bitonic, padded to a power of two), largest
@@ -236,6 +230,7 @@ __device__ __forceinline__ u64 block_scan(u64 v, Smem& s, u64& all) {
 // partners less than a warp apart by shuffles, the others through `a`. More: in
 // `a`, where a warp's 32 pairs of a stage lie in 64 entries of its own while
 // partners are at most 32 apart, so that those stages need no block barrier.
+template <int kThreads>
 __device__ __forceinline__ void block_sort(u64* a, int n, bool descending) {
   const int tid = threadIdx.x;
   int p = 64;
@@ -295,8 +290,9 @@ struct SampleParams {
   int cluster;    // CTAs per row
 };
 
-template <bool kBf16, bool kResident>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+template <int kThreads, bool kBf16, bool kResident>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleParams p) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(128) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);  // clusters are runs of C blocks
@@ -323,7 +319,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
   if (tid < kBins / 8) s.slice[0][tid] = s.slice[1][tid] = 0u;
   if (tid == 0) s.list_n = s.local_n = 0u;
-  const uint32_t lead_list = remote_addr(s.list, 0), lead_n = remote_addr(&s.list_n, 0);
 
   // ---- the row, once: logits (NaN as -inf, -0 as 0), their extremes, how many are in
   const char* row = static_cast<const char*>(p.logits) + (b * p.ld + i0) * (kBf16 ? 2 : 4);
@@ -416,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const auto cluster_sum = [&](Sums v) {
     v.a = warp_sum(v.a);
     v.b = warp_sum(v.b);
-    __syncthreads();
+    __syncthreads();  // v.c: one value per CTA
     if (lane == 0) {
       s.red[0][wid] = v.a;
       s.red[1][wid] = v.b;
@@ -426,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       v.a = warp_sum(lane < kWarps ? s.red[0][lane] : 0ull);
       v.b = warp_sum(lane < kWarps ? s.red[1][lane] : 0ull);
     }
-    exchange(v.a, v.b, 0ull);  // threads of warp 0 send
+    exchange(v.a, v.b, v.c);  // threads of warp 0 send
     return gather_sums();
   };
   uint32_t kmax, kmin;
@@ -508,7 +503,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const float reach = fminf((float)kTail * T, span);  // the bins' range, in x
   const bool tail_out = reach < span;                 // the last bin's weights are all zero
   const Bins whole{r.mxf, span > 0.0f ? (float)(kBins - 1) / reach : 1.0f};
-  const int packed = p.per <= kPackMax ? 18 : 0;
+  // A histogram word: a count above `packed` bits of a sum of 64ths of a bin (13 +
+  // 19 bits), of sixteenths where a CTA has more tokens (14 + 18), or a count alone.
+  const int packed = p.per <= kPackMax / 2 ? 19 : (p.per <= kPackMax ? 18 : 0);
+  const uint32_t drop = packed == 18 ? 2u : 0u;
 
   // The kept tokens so far: x > cut and the first `ties` with x == cut.
   float cut = -INFINITY;
@@ -516,32 +514,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   bool partial = true;  // more tokens than `ties` are at the cut
   bool by_k = kset > 0 && (uint32_t)kset < valid;
 
-  // Histogram of the tokens with lo <= x < hi (no upper end for a NaN) into the
-  // leader's totals. Each CTA adds up its share of the bins over the cluster: an
-  // atomic per bin and CTA on the leader took four times as long.
+  // Histogram of the tokens with lo <= x < hi (no upper end for a NaN), to every
+  // CTA. Each adds up its share of the bins over the cluster and sends it to all:
+  // an atomic per bin and CTA on one of them took four times as long, and with
+  // the row's histogram everywhere no verdict has to be sent around.
   const auto histogram = [&](const Bins& g, float lo, float hi) {
 #pragma unroll 4
     for (int i = tid; i < n; i += kThreads) {
       const float x = at(i);
       if (x >= lo && x > -INFINITY && !(x >= hi)) {
-        const uint32_t v = bin16(x, g);
-        atomicAdd(&s.hist[v >> 4], packed != 0 ? (1u << 18) + (v & 15u) : 1u);
+        const uint32_t v = bin64(x, g);
+        atomicAdd(&s.hist[v >> 6], packed != 0 ? (1u << packed) + ((v & 63u) >> drop) : 1u);
       }
     }
     cluster_sync();
     const int share = kBins / C;  // bins of this CTA
-    const int groups = share < kThreads ? kThreads / share : 1, sources = C / groups;  // C = 8, 16: 2, 4 groups
+    const int groups = share <= kBins / 8 ? kThreads / share : 1, sources = C / groups;  // several from 8 CTAs on
     for (int k = tid; k < share * groups; k += kThreads) {
       const int bin = rank * share + k % share, from = k / share * sources;
       uint32_t c = 0u, o = 0u;
       for (int q = 0; q < sources; ++q) {
         const uint32_t h = remote_load(remote_addr(&s.hist[bin], from + q));
-        c += packed != 0 ? h >> 18 : h;
-        o += packed != 0 ? h & 0x3FFFFu : 8u * h;
+        c += packed != 0 ? h >> packed : h;
+        o += packed != 0 ? h & ((1u << packed) - 1u) : h;
       }
       if (groups == 1) {
-        remote_store(remote_addr(&s.total.cnt[bin], 0), c);
-        remote_store(remote_addr(&s.total.off[bin], 0), o);
+        for (int q = 0; q < C; ++q) {
+          remote_store(remote_addr(&s.cnt[bin], q), c);
+          remote_store(remote_addr(&s.off[bin], q), o);
+        }
       } else if (c != 0u) {
         atomicAdd(&s.slice[0][k % share], c);
         atomicAdd(&s.slice[1][k % share], o);
@@ -549,11 +550,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     if (groups > 1) {
       __syncthreads();
-      if (tid < share) {
-        remote_store(remote_addr(&s.total.cnt[rank * share + tid], 0), s.slice[0][tid]);
-        remote_store(remote_addr(&s.total.off[rank * share + tid], 0), s.slice[1][tid]);
-        s.slice[0][tid] = s.slice[1][tid] = 0u;
+      for (int k = tid; k < share * C; k += kThreads) {
+        const int bin = k % share, to = k / share;
+        remote_store(remote_addr(&s.cnt[rank * share + bin], to), s.slice[0][bin]);
+        remote_store(remote_addr(&s.off[rank * share + bin], to), s.slice[1][bin]);
       }
+      __syncthreads();
+      if (tid < share) s.slice[0][tid] = s.slice[1][tid] = 0u;
     }
     cluster_sync();
   };
@@ -564,43 +567,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (tid == 0) s.local_n = 0u;
     __syncthreads();
   };
-  // The leader's verdict to every CTA.
-  const auto broadcast = [&]() {
-    __syncthreads();
-    if (rank == 0 && tid > 0 && tid < C) {
-      remote_store(remote_addr(&s.mode, tid), s.mode);
-      remote_store(remote_addr(&s.hi_key, tid), s.hi_key);
-      remote_store(remote_addr(&s.lo_key, tid), s.lo_key);
-      remote_store(remote_addr(&s.cut, tid), s.cut);
-      remote_store(remote_addr(&s.cut_partial, tid), s.cut_partial);
-      remote_store(remote_addr(&s.ties, tid), s.ties);
-      remote_store(remote_addr(&s.need, tid), s.need);
-    }
-    cluster_sync();
-  };
-  constexpr int kPerThread = kBins / kThreads;  // bins of a leader's thread, in order
+  constexpr int kPerThread = kBins / kThreads;  // neighbouring bins of a thread
   const auto collect = [&](int i, float x) {
     const uint32_t slot = atomicAdd(&s.local_n, 1u);
     if (slot < (uint32_t)kListMax) s.local[slot] = ((u64)sample_key(x) << 32) | (0xFFFFFFFFu - (uint32_t)(i0 + i));
   };
-  // This CTA's candidates to the leader's list; complete after a cluster barrier.
-  const auto flush = [&]() {
+  // This CTA's candidates to the lists of the first `to` CTAs; complete after a
+  // cluster barrier. Returns how many.
+  const auto flush = [&](int to) {
     __syncthreads();
     const uint32_t m = s.local_n < (uint32_t)kListMax ? s.local_n : (uint32_t)kListMax;
     if (m != 0u) {
-      if (tid == 0) s.base = remote_add(lead_n, m);
+      if (tid == 0) s.base = remote_add(remote_addr(&s.list_n, 0), m);
       __syncthreads();
-      const uint32_t to = s.base;
-      for (uint32_t i = tid; i < m && to + i < (uint32_t)kListMax; i += kThreads)
-        remote_store(lead_list + 8 * (to + i), s.local[i]);
+      const uint32_t at0 = s.base;
+      for (uint32_t k = tid; k < m * to; k += kThreads) {
+        const uint32_t i = k % m, q = k / m;
+        if (at0 + i < (uint32_t)kListMax) remote_store(remote_addr(&s.list[at0 + i], (int)q), s.local[i]);
+      }
     }
+    return (u64)m;
   };
-
-  // From the leader's list of candidates, which holds every kept token: apply
+  // From a list of m candidates, which holds every kept token: apply
   // top-k (keep), top-p (of row_total, or of the kept ones' sum) and min-p, and draw.
-  const auto draw_from_list = [&](int keep, bool use_p, bool own_total, u64 row_total) {
-    const int m = (int)s.list_n;
-    block_sort(s.list, m, true);
+  const auto draw_from_list = [&](int m, int keep, bool use_p, bool own_total, u64 row_total) {
+    block_sort<kThreads>(s.list, m, true);
     keep = keep < m ? keep : m;
     for (int i = tid; i < kListMax; i += kThreads)
       s.wlist[i] = i < keep ? key_weight((uint32_t)(s.list[i] >> 32), r, s.tab) : 0ull;
@@ -610,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       u64 w[kE], sum = 0, all;
 #pragma unroll
       for (int j = 0; j < kE; ++j) sum += w[j] = s.wlist[tid * kE + j];
-      u64 run = block_scan(sum, s, all);
+      u64 run = block_scan<kThreads>(sum, s, all);
       const double want = ceil(pp * (double)(own_total ? all : row_total));
       const u64 need = want > 1.0 ? (u64)want : 1ull;
 #pragma unroll
@@ -626,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       const uint32_t idx = 0xFFFFFFFFu - (uint32_t)s.list[i];
       s.list[i] = w == 0ull || w < wmin ? ~0ull : ((u64)idx << 32) | (uint32_t)i;
     }
-    block_sort(s.list, m, false);
+    block_sort<kThreads>(s.list, m, false);
     u64 w[kE], sum = 0, total;
 #pragma unroll
     for (int j = 0; j < kE; ++j) {
@@ -635,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       w[j] = e == ~0ull ? 0ull : s.wlist[(uint32_t)e];
       sum += w[j];
     }
-    u64 run = block_scan(sum, s, total);
+    u64 run = block_scan<kThreads>(sum, s, total);
     const u64 target = target_of(total);
 #pragma unroll
     for (int j = 0; j < kE; ++j) {
@@ -650,11 +641,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       run += w[j];
     }
   };
-  // From the leader's list of the tokens of consecutive bins: the border after
-  // the shortest run, largest first, of `need` tokens, or of weight `need`.
-  const auto settle = [&](u64 need, bool by_weight) {
-    const int m = (int)s.list_n;
-    block_sort(s.list, m, true);
+  // From a list of the m tokens of consecutive bins: the border after the
+  // shortest run, largest first, of `need` tokens, or of weight `need`. Every CTA
+  // has the list and comes to the same border.
+  const auto settle = [&](int m, u64 need, bool by_weight) {
+    block_sort<kThreads>(s.list, m, true);
     constexpr int kE = kListMax / kThreads;
     u64 w[kE], sum = 0, all;
 #pragma unroll
@@ -663,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       w[j] = i < m ? (by_weight ? key_weight((uint32_t)(s.list[i] >> 32), r, s.tab) : 1ull) : 0ull;
       sum += w[j];
     }
-    u64 run = block_scan(sum, s, all);
+    u64 run = block_scan<kThreads>(sum, s, all);
 #pragma unroll
     for (int j = 0; j < kE; ++j) {
       const int i = tid * kE + j;
@@ -682,12 +673,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       run += w[j];
     }
     __syncthreads();
-    if (tid == 0) s.list_n = 0u;
-  };
-  const auto take_cut = [&]() {
+    if (tid == 0) s.list_n = s.local_n = 0u;
     cut = key_value(s.cut);
     ties = s.ties;
     partial = s.cut_partial != 0u;
+    __syncthreads();
   };
   // The border without a list (more equal or near tokens than one holds):
   // bisection over the keys, a pass each. All CTAs take part and agree.
@@ -731,109 +721,127 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     ties = want;
   };
 
-  // Keys of the logits a bin's tokens have: [lo_key, hi_key), within [from, to).
-  const auto bin_range = [&](const Bins& g, uint32_t first, uint32_t last, uint32_t from, uint32_t to) {
-    // Two warps of the leader.
-    const uint32_t top = (to == 0xFFFFFFFFu ? r.top : to - 1u);  // lies in bin 0
+  // Keys of the logits in bins s.bin_lo .. s.bin_hi: [lo_key, hi_key), within [from, to).
+  const auto bin_range = [&](const Bins& g, uint32_t from, uint32_t to) {
+    const uint32_t top = to == 0xFFFFFFFFu ? r.top : to - 1u;  // lies in bin 0
+    const uint32_t below = from > kNoKey ? from - 1u : kNoKey;
     if (wid == 0) {
-      const uint32_t k = first == 0u ? to : bin_key(first, g, from > kNoKey ? from - 1u : kNoKey, top);
+      const uint32_t k = s.bin_lo == 0 ? to : bin_key((uint32_t)s.bin_lo, g, below, top);
       if (lane == 0) s.hi_key = k;
     } else if (wid == 1) {
-      const uint32_t k = last == kBins - 1 ? from : bin_key(last + 1u, g, from > kNoKey ? from - 1u : kNoKey, top);
+      const uint32_t k = s.bin_hi == kBins - 1 ? from : bin_key((uint32_t)s.bin_hi + 1u, g, below, top);
       if (lane == 0) s.lo_key = k;
     }
     __syncthreads();
   };
-  // Leader: the bin of the need-th token of a histogram, and what to do about it.
-  const auto place_count = [&](const Bins& g, u64 need, bool may_whole, uint32_t from, uint32_t to) {
+  // The bin of the need-th token of the histogram, and what to do about it.
+  const auto place_count = [&](u64 need, bool may_whole) {
     u64 mine[kPerThread], sum = 0, all;
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) sum += mine[j] = s.total.cnt[tid * kPerThread + j];
-    u64 run = block_scan(sum, s, all);
+    for (int j = 0; j < kPerThread; ++j) sum += mine[j] = s.cnt[tid * kPerThread + j];
+    u64 run = block_scan<kThreads>(sum, s, all);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       if (run < need && run + mine[j] >= need) {
         const int bin = tid * kPerThread + j;
-        s.mode = may_whole && run + mine[j] <= kListMax               ? kWhole
+        s.mode = may_whole && run + mine[j] <= (by_p ? 2 : 1) * kWholeMax ? kWhole
                  : mine[j] <= kListMax                                ? kBorder
                  : may_whole && bin == kBins - 1 && tail_out          ? kZeros
                                                                       : kCrowd;
         s.bin_hi = bin;
         s.bin_lo = s.mode == kWhole ? 0 : bin;
         s.need = need - run;  // how many of the bin's tokens stay
-        s.ties = mine[j];          // of how many
+        s.count = mine[j];    // of how many
       }
       run += mine[j];
     }
     __syncthreads();
-    bin_range(g, s.bin_lo, s.bin_hi, from, to);
   };
-  // Leader: the bins in which a running weight meets a target, by bounds of every
+  // The bins in which a running weight meets a target, by bounds of every
   // bin's weight: a token f bins past the bin's start weighs e^(-delta f) of it,
-  // between 1 - delta f and the chord; f is known to half a sixteenth (and the
-  // rounding of the bin position, below 0.01 bins), or not at all without
-  // the sixteenths. `first` is the weight at the bins' origin. The target is
+  // between 1 - delta f and the chord; f is known to half a step of the
+  // histogram's sums and the rounding of the bin position (three of 2^-24 of 2047 bins, under 0.002). `first` is the weight at the bins' origin. The target is
   // share * total (target < 0) or a weight. In fp32, whose errors over 2048
-  // additions stay below the 1e-5 that the borders are widened by.
-  const auto place_weight = [&](const Bins& g, float first, float target, bool may_whole, uint32_t from, uint32_t to,
-                                bool open_end) {
+  // additions stay below the 2e-5 that the borders are widened by.
+  const auto place_weight = [&](const Bins& g, float first, float target, bool may_whole, bool open_end) {
     // Exponent per bin (no bins to speak of where all tokens are equal or T is infinite).
-    const float delta = g.scale < INFINITY && inv_t > 0.0 ? fminf((float)(inv_t / (double)g.scale), 1.0f) : 0.0f;
-    const float fe = packed != 0 ? 1.0f / 32.0f + 0.01f : 0.51f;
+    const float inv_tf = (float)inv_t;
+    const float delta = g.scale < INFINITY && inv_tf > 0.0f ? fminf(inv_tf / g.scale, 1.0f) : 0.0f;
+    // The mean place of a word's step and how far from it a token may be, in bins.
+    const float unit = packed == 19 ? 1.0f / 64.0f : (packed == 18 ? 1.0f / 16.0f : 0.0f);
+    const float mid = packed == 19 ? 0.0f : (packed == 18 ? 1.5f / 64.0f : 0.5f);
+    const float fe = (packed == 19 ? 0.5f / 64.0f : (packed == 18 ? 2.0f / 64.0f : 0.5f)) + 0.002f;
     const float shrink = delta * (1.0f - delta * (0.5f - delta * (1.0f / 6.0f)));
     const float step = expf(-delta);
     float e = first * expf(-delta * (float)(tid * kPerThread));
     float lo[kPerThread], hi[kPerThread], slo = 0.f, shi = 0.f;
-    u64 mine[kPerThread], cnt = 0, all;
-    const uint32_t cut_bin = cut > -INFINITY && partial ? bin16(cut, g) >> 4 : 0xFFFFFFFFu;
+    uint32_t mine[kPerThread], cnt = 0;
+    const uint32_t cut_bin = cut > -INFINITY && partial ? bin64(cut, g) >> 6 : 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const int bin = tid * kPerThread + j;
-      cnt += mine[j] = s.total.cnt[bin];
-      const float c = (float)mine[j], f = (float)s.total.off[bin] * (1.0f / 16.0f);
+      cnt += mine[j] = s.cnt[bin];
+      const float c = (float)mine[j], f = (float)s.off[bin] * unit + c * mid;
       const float slack = c * 1e-12f;  // the rounding to 2^-40
       lo[j] = c > 0.f ? fmaxf(e * (c - delta * (f + c * fe)) - slack, 0.f) : 0.f;
-      hi[j] = c > 0.f ? e * (c - shrink * fmaxf(f - c * fe, 0.f)) * (1.0f + delta * delta + 0.1f * delta) + slack : 0.f;
+      hi[j] = c > 0.f ? e * (c - shrink * fmaxf(f - c * fe, 0.f)) * (1.0f + delta * delta) + slack : 0.f;
       if ((open_end && bin == kBins - 1) || (uint32_t)bin == cut_bin) lo[j] = 0.f;
       slo += lo[j];
       shi += hi[j];
       e *= step;
     }
-    float plo = slo, phi = shi;  // prefixes of both
+    float plo = slo, phi = shi;  // prefixes of both, and of the counts
+    uint32_t run = cnt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const float x = __shfl_up_sync(0xFFFFFFFFu, plo, d), y = __shfl_up_sync(0xFFFFFFFFu, phi, d);
+      const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, run, d);
       if (lane >= d) {
         plo += x;
         phi += y;
+        run += z;
       }
     }
     if (lane == 31) {
       s.redf[0][wid] = plo;
       s.redf[1][wid] = phi;
+      s.red[0][wid] = run;
     }
     if (tid == 0) s.bin_lo = s.bin_hi = kBins - 1;
-    u64 run = block_scan(cnt, s, all);  // its barriers order the lines around it
-    float tlo = 0.f, thi = 0.f;
-    plo -= slo;
-    phi -= shi;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < wid) {
-        plo += s.redf[0][i];
-        phi += s.redf[1][i];
+    __syncthreads();
+    float wlo = lane < kWarps ? s.redf[0][lane] : 0.f, whi = lane < kWarps ? s.redf[1][lane] : 0.f;
+    uint32_t wrun = lane < kWarps ? (uint32_t)s.red[0][lane] : 0u;
+#pragma unroll
+    for (int d = 1; d < kWarps; d <<= 1) {
+      const float x = __shfl_up_sync(0xFFFFFFFFu, wlo, d), y = __shfl_up_sync(0xFFFFFFFFu, whi, d);
+      const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, wrun, d);
+      if (lane >= d) {
+        wlo += x;
+        whi += y;
+        wrun += z;
       }
-      tlo += s.redf[0][i];
-      thi += s.redf[1][i];
     }
+    const float tlo = __shfl_sync(0xFFFFFFFFu, wlo, kWarps - 1), thi = __shfl_sync(0xFFFFFFFFu, whi, kWarps - 1);
+    const int prev = wid > 0 ? wid - 1 : 0;
+    const float blo_f = __shfl_sync(0xFFFFFFFFu, wlo, prev), bhi_f = __shfl_sync(0xFFFFFFFFu, whi, prev);
+    const uint32_t brun = __shfl_sync(0xFFFFFFFFu, wrun, prev);
+    plo += (wid > 0 ? blo_f : 0.f) - slo;
+    phi += (wid > 0 ? bhi_f : 0.f) - shi;
+    run += (wid > 0 ? brun : 0u) - cnt;
+    int first_lo = kBins - 1, first_hi = kBins - 1;
     const float want_lo = target < 0.f ? (float)pp * tlo : target, want_hi = target < 0.f ? (float)pp * thi : target;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const int bin = tid * kPerThread + j;
-      if ((phi + hi[j]) * (1.0f + 1e-5f) >= want_lo * (1.0f - 1e-5f)) atomicMin(&s.bin_lo, bin);
-      if ((plo + lo[j]) * (1.0f - 1e-5f) >= want_hi * (1.0f + 1e-5f)) atomicMin(&s.bin_hi, bin);
+      if ((phi + hi[j]) * (1.0f + 2e-5f) >= want_lo * (1.0f - 2e-5f)) first_lo = min(first_lo, bin);
+      if ((plo + lo[j]) * (1.0f - 2e-5f) >= want_hi * (1.0f + 2e-5f)) first_hi = min(first_hi, bin);
       plo += lo[j];
       phi += hi[j];
     }
+    first_lo = __reduce_min_sync(0xFFFFFFFFu, first_lo);
+    first_hi = __reduce_min_sync(0xFFFFFFFFu, first_hi);
+    if (lane == 0 && first_lo < kBins - 1) atomicMin(&s.bin_lo, first_lo);
+    if (lane == 0 && first_hi < kBins - 1) atomicMin(&s.bin_hi, first_hi);
     __syncthreads();
     const int blo = s.bin_lo, bhi = s.bin_hi;
 #pragma unroll
@@ -844,13 +852,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       run += mine[j];
     }
     __syncthreads();
-    const u64 before = s.red[1][0], through = s.red[1][1];
-    const uint32_t mode = may_whole && through <= kListMax ? kWhole : (through - before <= kListMax ? kBorder : kCrowd);
+    const uint32_t before = (uint32_t)s.red[1][0], through = (uint32_t)s.red[1][1];
+    const uint32_t mode = may_whole && through <= kWholeMax ? kWhole : (through - before <= kListMax ? kBorder : kCrowd);
     if (tid == 0) {
       s.mode = mode;
-      s.ties = through - before;
+      s.count = through - before;
+      if (mode == kWhole) s.bin_lo = 0;
     }
-    bin_range(g, mode == kWhole ? 0u : (uint32_t)blo, (uint32_t)bhi, from, to);
+    __syncthreads();
   };
   // The border among the `count` tokens of keys [lk, hk), more than a list holds:
   // finer bins over that range, until a list holds a bin's tokens or all have one
@@ -875,16 +884,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       const float hi_x = hk == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(hk);
       clear_histogram();
       histogram(g, lo_v, hi_x);
-      if (rank == 0) {
-        if (by_weight)
-          place_weight(g, (float)((double)key_weight(last, r, s.tab) / kWeightOne), (float)((double)need / kWeightOne),
-                       false, lk, hk, false);
-        else
-          place_count(g, need, false, lk, hk);
-      }
-      broadcast();
+      if (by_weight)
+        place_weight(g, (float)((double)key_weight(last, r, s.tab) / kWeightOne), (float)((double)need / kWeightOne),
+                     false, false);
+      else
+        place_count(need, false);
+      bin_range(g, lk, hk);
       const uint32_t mode = s.mode, nlk = s.lo_key, nhk = s.hi_key;
-      count = s.ties;
+      count = s.count;
       const u64 in_bin = s.need;
       const bool list = mode == kBorder;
       Sums v = {0, 0, 0};
@@ -895,13 +902,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (key >= nhk) v.b += by_weight ? weight(x, r, s.tab) : 0ull;
         else if (list) collect(i, x);
       }
-      if (list) flush();
+      if (list) v.c = flush(C);
       v = cluster_sum(v);
       need = by_weight ? need - v.b : in_bin;
       if (list) {
-        if (rank == 0) settle(need, by_weight);
-        broadcast();
-        take_cut();
+        settle((int)v.c, need, by_weight);
         return true;
       }
       if (nlk == lk && nhk == hk) break;
@@ -914,28 +919,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // ---- top-k
   if (by_k) {
     histogram(whole, -INFINITY, __uint_as_float(0x7FC00000u));
-    if (rank == 0) place_count(whole, (u64)kset, true, 1u, 0xFFFFFFFFu);
-    broadcast();
-    const uint32_t mode = s.mode, hk = s.hi_key, lk = s.lo_key;
-    const u64 in_bin = s.need, count = s.ties;
+    place_count((u64)kset, true);
+    const uint32_t mode = s.mode, b0 = (uint32_t)s.bin_lo, b1 = (uint32_t)s.bin_hi;
+    const u64 in_bin = s.need, count = s.count;
     if (mode == kWhole || mode == kBorder) {
 #pragma unroll 4
       for (int i = tid; i < n; i += kThreads) {
         const float x = at(i);
-        const uint32_t key = sample_key(x);
-        if (key >= lk && key < hk) collect(i, x);
+        const uint32_t bin = bin64(x, whole) >> 6;
+        if (x > -INFINITY && bin >= b0 && bin <= b1) collect(i, x);
       }
-      flush();
-      cluster_sync();
+      const u64 m = cluster_sum(Sums{0, 0, flush(mode == kWhole ? 1 : C)}).c;
       if (mode == kWhole) {
-        if (rank == 0) draw_from_list(kset, by_p, true, 0ull);
+        if (rank == 0) draw_from_list((int)m, kset, by_p, true, 0ull);
         return;
       }
-      if (rank == 0) settle(in_bin, false);
-      broadcast();
-      take_cut();
-    } else if (mode == kCrowd && !zoom(in_bin, false, lk, hk, count)) {
-      bisect((u64)kset, false);
+      settle((int)m, in_bin, false);
+    } else if (mode == kCrowd) {
+      bin_range(whole, 1u, 0xFFFFFFFFu);
+      if (!zoom(in_bin, false, s.lo_key, s.hi_key, count)) bisect((u64)kset, false);
     }
     if (by_p) clear_histogram();  // again, of what is left
   }
@@ -946,18 +948,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int own = ((n + kThreads - 1) / kThreads) | 1;
   const int t0 = own * tid < n ? own * tid : n, t1 = t0 + own < n ? t0 + own : n;
   u64 sure = 0;           // weight of the thread's tokens that are kept whatever the border
-  float sure_from = __uint_as_float(0x7FC00000u);  // those x >= it (none, for a NaN)
+  uint32_t sure_to = 0u;  // those at places before this one
 
   // ---- top-p
   if (by_p) {
     histogram(whole, cut, __uint_as_float(0x7FC00000u));
-    if (rank == 0) place_weight(whole, 1.0f, -1.0f, true, 1u, 0xFFFFFFFFu, true);
-    broadcast();
-    const uint32_t mode = s.mode, hk = s.hi_key, lk = s.lo_key;
-    const u64 count = s.ties;
-    // Candidates: lo_x <= x < hi_x; kept whatever the border: x >= hi_x (never, for a NaN).
-    const float hi_x = hk == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(hk);
-    const float lo_x = lk <= kNoKey ? -INFINITY : key_value(lk);
+    place_weight(whole, 1.0f, -1.0f, true, true);
+    const uint32_t mode = s.mode;
+    const u64 count = s.count;
+    sure_to = (uint32_t)s.bin_lo << 6;  // kept whatever the border: places before it
+    const uint32_t to = ((uint32_t)s.bin_hi + 1u) << 6;  // candidates: places from there to here
     // One pass with an exponential per token: the sum of all kept tokens, of
     // those above the candidates, and the candidates. A sum of weight bits holds
     // kMagicBits once per token, taken off at the end; the largest logit
@@ -972,32 +972,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       w = inf ? 0ull : w;
       w = x == r.mxf ? 1ull << 40 : w;
       w = x >= cut ? w : 0ull;
-      const bool above = x >= hi_x;
+      const uint32_t place = bin64(x, whole);
+      const bool above = place < sure_to;
       v.a += partial && x == cut ? 0ull : w;  // a tie of top-k's border is counted by its rank
       v.b += above ? w : 0ull;
       sure += above && w >= wmin ? w : 0ull;
-      if (list && !above && x >= lo_x && x >= cut && x > -INFINITY) collect(i, x);
+      if (list && !above && place < to && x >= cut && x > -INFINITY) collect(i, x);
     }
-    if (list) flush();
+    if (list) v.c = flush(mode == kWhole ? 1 : C);
     v = cluster_sum(v);  // its barrier also completes the list
     const u64 total = v.a + (partial && ties > 0 ? ties * weight(cut, r, s.tab) : 0ull);
     const double want = ceil(pp * (double)total);
     const u64 need = want > 1.0 ? (u64)want : 1ull;
     if (mode == kWhole) {
       // All that can stay is in the list; top-k's border cuts it at kset tokens.
-      if (rank == 0) draw_from_list(by_k ? kset : kListMax, true, false, total);
+      if (rank == 0) draw_from_list((int)v.c, by_k ? kset : kListMax, true, false, total);
       return;
     }
     if (mode == kBorder) {
-      if (rank == 0) settle(need - v.b, true);
-      broadcast();
-      take_cut();
-      sure_from = hi_x;
-    } else if (zoom(need - v.b, true, lk, hk, count)) {
-      sure_from = hi_x;
+      settle((int)v.c, need - v.b, true);
     } else {
-      bisect(need, true);
-      sure = 0;
+      bin_range(whole, 1u, 0xFFFFFFFFu);
+      if (!zoom(need - v.b, true, s.lo_key, s.hi_key, count)) {
+        bisect(need, true);
+        sure = 0;
+        sure_to = 0u;
+      }
     }
   }
 
@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (ranked) {
     u64 mine = 0, all;
     for (int i = t0; i < t1; ++i) mine += at(i) == cut ? 1 : 0;
-    tie = block_scan(mine, s, all);
+    tie = block_scan<kThreads>(mine, s, all);
     exchange(all, 0, 0);
     gather_sums();
     tie += before_me;
@@ -1021,13 +1021,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll 4
   for (int i = t0; i < t1; ++i) {
     const float x = at(i);
-    if (x >= cut && !(x >= sure_from)) {
+    if (x >= cut && bin64(x, whole) >= sure_to) {
       sum += kept_weight(x, tr);
       if (x == cut) ++tr;
     }
   }
   u64 mine_all;
-  u64 run = block_scan(sum, s, mine_all);
+  u64 run = block_scan<kThreads>(sum, s, mine_all);
   exchange(mine_all, 0, 0);
   const u64 total = gather_sums().a, target = target_of(total);
   run += before_me;
@@ -1055,10 +1055,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
 }
 
-template <bool kBf16, bool kResident>
+template <int kThreads, bool kBf16, bool kResident>
 cudaError_t launch_sample_t(const SampleParams& p, int64_t B, int C, size_t smem, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
-  auto kern = sample_kernel<kBf16, kResident>;
+  auto kern = sample_kernel<kThreads, kBf16, kResident>;
   cudaError_t e = allow_smem(kern, kSampleSmemMax, allowed);
   if (e != cudaSuccess) return e;
   if (C > 8) {  // more CTAs than every device has to support
@@ -1114,10 +1114,17 @@ cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, i
     q.u += b;
     q.tokens += b;
     if (logprobs != nullptr) q.logprobs += b;
-    const cudaError_t e = bf16 ? (resident ? launch_sample_t<true, true>(q, part, C, smem, stream)
-                                           : launch_sample_t<true, false>(q, part, C, smem, stream))
-                               : (resident ? launch_sample_t<false, true>(q, part, C, smem, stream)
-                                           : launch_sample_t<false, false>(q, part, C, smem, stream));
+    // A launch that gives every SM one CTA at most takes the wide ones.
+    const bool wide = part * C <= num_sms;
+    cudaError_t e;
+    if (bf16)
+      e = !resident ? launch_sample_t<512, true, false>(q, part, C, smem, stream)
+          : wide    ? launch_sample_t<1024, true, true>(q, part, C, smem, stream)
+                    : launch_sample_t<512, true, true>(q, part, C, smem, stream);
+    else
+      e = !resident ? launch_sample_t<512, false, false>(q, part, C, smem, stream)
+          : wide    ? launch_sample_t<1024, false, true>(q, part, C, smem, stream)
+                    : launch_sample_t<512, false, true>(q, part, C, smem, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
