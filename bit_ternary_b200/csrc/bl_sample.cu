@@ -141,9 +141,7 @@ __device__ const Exp2Table kExp2Table = make_exp2_table();
 // The result is 2^52 + w as a double's bits: kMagicBits less is w, and sums of
 // such bits, modulo 2^64, are sums of weights and counts of kMagicBits.
 constexpr u64 kMagicBits = 0x4330000000000000ull;  // 2^52
-__device__ __forceinline__ u64 weight_bits(float x, const Row& r, const double* tab) {
-  double t = (r.mx - (double)x) * r.c;
-  t = fmax(t, -256.0 * 64.0);
+__device__ __forceinline__ u64 weight_bits_at(double t, const double* tab) {  // t: 256ths of an octave, > -2^14
   const double magic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
   const double tm = t + magic;
   const int n = __double2loint(tm);
@@ -154,6 +152,13 @@ __device__ __forceinline__ u64 weight_bits(float x, const Row& r, const double* 
   v = fma(v, q, v);
   v = __hiloint2double(__double2hiint(v) + ((n & ~255) << 12), __double2loint(v));  // times 2^(n >> 8)
   return (u64)__double_as_longlong(v + 4503599627370496.0);
+}
+__device__ __forceinline__ u64 weight_bits(float x, const Row& r, const double* tab) {
+  return weight_bits_at(fmax((r.mx - (double)x) * r.c, -256.0 * 63.0), tab);
+}
+// As weight_bits for x within 44 T of the largest logit (44 log2(e) < 64 octaves).
+__device__ __forceinline__ u64 weight_bits_near(float x, const Row& r, const double* tab) {
+  return weight_bits_at((r.mx - (double)x) * r.c, tab);
 }
 __device__ __forceinline__ u64 weight(float x, const Row& r, const double* tab) {
   if (x == r.mxf) return 1ull << 40;
@@ -237,24 +242,26 @@ __device__ __forceinline__ void block_sort(u64* a, int n, bool descending) {
   while (p < n) p <<= 1;
   __syncthreads();
   if (p <= kThreads) {
+    const bool mine = tid < p;  // whole warps
     u64 x = tid < n ? a[tid] : (descending ? 0ull : ~0ull);
+    const auto keep = [&](u64 y, int k, int j) {
+      const bool small = ((tid & k) == 0) == ((tid & j) == 0);
+      x = (x > y) == (small != descending) ? y : x;
+    };
     for (int k = 2; k <= p; k <<= 1) {
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        u64 y;
-        if (j >= 32) {
-          __syncthreads();
-          if (tid < p) a[tid] = x;
-          __syncthreads();
-          y = tid < p ? a[tid ^ j] : x;
-        } else {
-          y = __shfl_xor_sync(0xFFFFFFFFu, x, j);
-        }
-        const bool keep_small = ((tid & k) == 0) == ((tid & j) == 0);
-        x = (x > y) == (keep_small != descending) ? y : x;
+      int j = k >> 1;
+      for (; j >= 32; j >>= 1) {
+        __syncthreads();
+        if (mine) a[tid] = x;
+        __syncthreads();
+        if (mine) keep(a[tid ^ j], k, j);
+      }
+      if (mine) {
+        for (; j > 0; j >>= 1) keep(__shfl_xor_sync(0xFFFFFFFFu, x, j), k, j);
       }
     }
     __syncthreads();
-    if (tid < p) a[tid] = x;
+    if (mine) a[tid] = x;
     __syncthreads();
     return;
   }
@@ -305,17 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // below, before the first exchange.
   cluster_arrive();
 
-  // ---- settings of the row, and what later passes start from
+  // ---- settings of the row (used after the row's loads are under way), and what
+  // later passes start from
   const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;
   const int kset = p.how.top_k != nullptr ? p.how.top_k[b] : p.how.top_k_value;
   const float pset = p.how.top_p != nullptr ? p.how.top_p[b] : p.how.top_p_value;
   const float mset = p.how.min_p != nullptr ? p.how.min_p[b] : p.how.min_p_value;
-  const bool greedy = !(T > 0.0f);
-  const bool by_p = pset < 1.0f;  // false for NaN
-  const double pp = pset > 0.0f ? (double)pset : 0.0;
-  const u64 wmin = mset > 0.0f ? (u64)ceil((mset < 1.0f ? (double)mset : 1.0) * kWeightOne) : 0ull;
-
-  if (tid < 128) reinterpret_cast<double2*>(s.tab)[tid] = reinterpret_cast<const double2*>(kExp2Table.v)[tid];
+  double2 tab2 = make_double2(0.0, 0.0);
+  if (tid < 128) tab2 = __ldg(reinterpret_cast<const double2*>(kExp2Table.v) + tid);
   for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
   if (tid < kBins / 8) s.slice[0][tid] = s.slice[1][tid] = 0u;
   if (tid == 0) s.list_n = s.local_n = 0u;
@@ -381,6 +385,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   } else {
     for (int i = tid; i < n; i += kThreads) note(load(i));
   }
+
+  const bool greedy = !(T > 0.0f);
+  const bool by_p = pset < 1.0f;  // false for NaN
+  const double pp = pset > 0.0f ? (double)pset : 0.0;
+  const u64 wmin = mset > 0.0f ? (u64)ceil((mset < 1.0f ? (double)mset : 1.0) * kWeightOne) : 0ull;
+
+  if (tid < 128) reinterpret_cast<double2*>(s.tab)[tid] = tab2;
 
   // Three values of every CTA to all CTAs; one cluster barrier. The two buffers
   // alternate, so a CTA writes a buffer again only after every reader of it
@@ -963,21 +974,48 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     // kMagicBits once per token, taken off at the end; the largest logit
     // and those beside an infinite one take no exponential.
     Sums v = {0, 0, 0};
-    const bool inf = r.mxf == INFINITY;
     const bool list = mode != kCrowd;
+    const float floor_x = r.mxf - 44.0f * T;  // weights from here down are zero
+    if (wmin == 0 && r.mxf < INFINITY && floor_x > -0x1p126f && r.mxf - floor_x >= 30.0f * T) {
+      // The usual settings (44 T is above the rounding of the largest logit): what is not kept weighs what floor_x does, nothing.
+      // Sums of weight bits hold kMagicBits once per token, taken off at the end.
+      const float first = cut > -INFINITY ? (partial ? nextafterf(cut, INFINITY) : cut) : floor_x;
+      const int above_to = (int)(0x4B000000u + sure_to);  // a place as bits of 2^23 + place
+      const int list_to = list ? (int)(0x4B000000u + to) : 0;
+      u64 all_bits = 0, above_bits = 0;
+      uint32_t above_n = 0;
 #pragma unroll 4
-    for (int i = t0; i < t1; ++i) {
-      const float x = at(i);
-      u64 w = weight_bits(x, r, s.tab) - kMagicBits;  // of -inf: zero
-      w = inf ? 0ull : w;
-      w = x == r.mxf ? 1ull << 40 : w;
-      w = x >= cut ? w : 0ull;
-      const uint32_t place = bin64(x, whole);
-      const bool above = place < sure_to;
-      v.a += partial && x == cut ? 0ull : w;  // a tie of top-k's border is counted by its rank
-      v.b += above ? w : 0ull;
-      sure += above && w >= wmin ? w : 0ull;
-      if (list && !above && place < to && x >= cut && x > -INFINITY) collect(i, x);
+      for (int i = t0; i < t1; ++i) {
+        const float x = at(i);
+        const float y = fmaxf(x >= first ? x : floor_x, floor_x);
+        const u64 w = weight_bits_near(y, r, s.tab);
+        all_bits += w;
+        const float pos = fminf((whole.origin - x) * whole.scale, (float)(kBins - 1));
+        const int place = x == whole.origin ? 0x4B000000 : __float_as_int(fmaf(pos, 64.0f, 8388608.0f));
+        if (place < above_to) {
+          above_bits += w;
+          ++above_n;
+        } else if (place < list_to && x >= cut && x > -INFINITY) {
+          collect(i, x);
+        }
+      }
+      v.a = all_bits - (u64)(t1 - t0) * kMagicBits;
+      sure = v.b = above_bits - (u64)above_n * kMagicBits;
+    } else {
+      const bool inf = r.mxf == INFINITY;
+      for (int i = t0; i < t1; ++i) {
+        const float x = at(i);
+        u64 w = weight_bits(x, r, s.tab) - kMagicBits;  // of -inf: zero
+        w = inf ? 0ull : w;
+        w = x == r.mxf ? 1ull << 40 : w;
+        w = x >= cut ? w : 0ull;
+        const uint32_t place = bin64(x, whole);
+        const bool above = place < sure_to;
+        v.a += partial && x == cut ? 0ull : w;  // a tie of top-k's border is counted by its rank
+        v.b += above ? w : 0ull;
+        sure += above && w >= wmin ? w : 0ull;
+        if (list && !above && place < to && x >= cut && x > -INFINITY) collect(i, x);
+      }
     }
     if (list) v.c = flush(mode == kWhole ? 1 : C);
     v = cluster_sum(v);  // its barrier also completes the list
