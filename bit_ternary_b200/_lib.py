@@ -27,10 +27,26 @@ STATUS_NAMES = {
     9: "BL_ERR_FORMAT",
 }
 
+class Sampling(ctypes.Structure):
+    """Mirror of bl_sampling (include/bitlinear.h)."""
+
+    _fields_ = [
+        ("temperature", ctypes.c_void_p),
+        ("top_k", ctypes.c_void_p),
+        ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
+        ("temperature_value", ctypes.c_float),
+        ("top_k_value", ctypes.c_int32),
+        ("top_p_value", ctypes.c_float),
+        ("min_p_value", ctypes.c_float),
+    ]
+
+
 # name -> (restype, argtypes), mirroring include/bitlinear.h
 _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_SAMPLING = ctypes.POINTER(Sampling)
 SIGNATURES = {
     "bitlinear_abi_version": (ctypes.c_int, []),
     "bitlinear_build_id": (ctypes.c_char_p, []),
@@ -89,13 +105,13 @@ SIGNATURES = {
                                             _VP]),
     "bitlinear_forward_w4_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP,
                                                  _SZ, _VP]),
-    "bitlinear_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
-    "bitlinear_sample_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    "bitlinear_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, _SAMPLING, _VP, _VP, _VP, _VP]),
+    "bitlinear_sample_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, _SAMPLING, _VP, _VP, _VP, _VP]),
     "bitlinear_w4_sample_workspace_size": (_SZ, [_I64, _I64, _I64]),
-    "bitlinear_forward_w4_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP,
-                                                   _VP, _VP, _VP, _SZ, _VP]),
-    "bitlinear_forward_w4_sample_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _VP,
-                                                        _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "bitlinear_forward_w4_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP, _SAMPLING,
+                                                   _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "bitlinear_forward_w4_sample_bf16": (ctypes.c_int, [_VP, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _VP,
+                                                        _SAMPLING, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "bitlinear_workspace_error": (ctypes.c_int, [_VP, _SZ, _VP]),
     "bitlinear_selftest_wait_timeout": (ctypes.c_int, [_VP, _SZ, ctypes.c_uint64, _VP]),
     "bitlinear_forward_noalloc": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP]),
@@ -118,21 +134,6 @@ class LinearCall(ctypes.Structure):
         ("packed", ctypes.c_void_p),
         ("D", ctypes.c_void_p),
         ("y", ctypes.c_void_p),
-    ]
-
-
-class Sampling(ctypes.Structure):
-    """Mirror of bl_sampling (include/bitlinear.h)."""
-
-    _fields_ = [
-        ("temperature", ctypes.c_void_p),
-        ("top_k", ctypes.c_void_p),
-        ("top_p", ctypes.c_void_p),
-        ("min_p", ctypes.c_void_p),
-        ("temperature_value", ctypes.c_float),
-        ("top_k_value", ctypes.c_int32),
-        ("top_p_value", ctypes.c_float),
-        ("min_p_value", ctypes.c_float),
     ]
 
 
@@ -185,5 +186,6 @@ def check(fn: str, status: int) -> None:
 def call(fn: str, *args) -> int:
     """Call an int-returning entry point and raise on a non-OK status."""
     st = getattr(lib(), fn)(*args)
-    check(fn, st)
+    if st != BL_OK:
+        check(fn, st)
     return st

@@ -9,7 +9,6 @@ the page read out of bounds).
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
@@ -414,7 +413,8 @@ def _w4_input(x: torch.Tensor, w: W4Weights) -> str:
     sfx = _float_input(x, "x")
     if x.dim() != 2 or x.shape[1] != w.in_features:
         raise ValueError(f"x must be [M, {w.in_features}], got {list(x.shape)}")
-    _same_device(x, "x", w.device)
+    if x.device != w.device:
+        _same_device(x, "x", w.device)
     return sfx
 
 
@@ -441,26 +441,33 @@ def forward_w4(x: torch.Tensor, w: W4Weights, out: Optional[torch.Tensor] = None
     return y
 
 
+def _setting(v: torch.Tensor, name: str, dtype: torch.dtype, B: int, device: torch.device) -> int:
+    if v.dtype is not dtype or v.device != device or not v.is_contiguous() or v.numel() != B:
+        _need_cuda(v, name, dtype)
+        _same_device(v, name, device)
+        raise ValueError(f"{name} must hold one value per row ({B}), got {v.numel()}")
+    return v.data_ptr()
+
+
 def _sampling(B: int, device: torch.device, temperature, top_k, top_p, min_p) -> "_lib.Sampling":
     how = _lib.Sampling()
-    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if isinstance(v, torch.Tensor):
-            _need_cuda(v, name, dtype)
-            _same_device(v, name, device)
-            if v.numel() != B:
-                raise ValueError(f"{name} must hold one value per row ({B}), got {v.numel()}")
-            setattr(how, name, v.data_ptr())
-        else:
-            setattr(how, name + "_value", v)
+    if isinstance(temperature, torch.Tensor):
+        how.temperature = _setting(temperature, "temperature", torch.float32, B, device)
+    else:
+        how.temperature_value = temperature
+    if isinstance(top_k, torch.Tensor):
+        how.top_k = _setting(top_k, "top_k", torch.int32, B, device)
+    else:
+        how.top_k_value = top_k
+    if isinstance(top_p, torch.Tensor):
+        how.top_p = _setting(top_p, "top_p", torch.float32, B, device)
+    else:
+        how.top_p_value = top_p
+    if isinstance(min_p, torch.Tensor):
+        how.min_p = _setting(min_p, "min_p", torch.float32, B, device)
+    else:
+        how.min_p_value = min_p
     return how
-
-
-def _need_u(u: torch.Tensor, B: int, device: torch.device) -> None:
-    _need_cuda(u, "u", torch.float32)
-    _same_device(u, "u", device)
-    if u.numel() != B:
-        raise ValueError(f"u must hold one number per row ({B}), got {u.numel()}")
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0,
@@ -482,13 +489,13 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     ld = logits.stride(0) if B > 1 else V
     if ld < V:
         raise ValueError("the rows of logits must not overlap")
-    _need_u(u, B, logits.device)
-    how = _sampling(B, logits.device, temperature, top_k, top_p, min_p)
-    tokens = torch.empty(B, dtype=torch.int64, device=logits.device)
-    logprobs = torch.empty(B, dtype=torch.float32, device=logits.device)
-    sfx = "_bf16" if logits.dtype == torch.bfloat16 else ""
-    _call_on(logits.device, "bitlinear_sample" + sfx, logits.data_ptr(), B, V, ld, ctypes.byref(how), u.data_ptr(),
-             tokens.data_ptr(), logprobs.data_ptr())
+    device = logits.device
+    u_ptr = _setting(u, "u", torch.float32, B, device)
+    how = _sampling(B, device, temperature, top_k, top_p, min_p)
+    tokens = torch.empty(B, dtype=torch.int64, device=device)
+    logprobs = torch.empty(B, dtype=torch.float32, device=device)
+    fn = "bitlinear_sample_bf16" if logits.dtype == torch.bfloat16 else "bitlinear_sample"
+    _call_on(device, fn, logits.data_ptr(), B, V, ld, how, u_ptr, tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs
 
 
@@ -498,15 +505,15 @@ def forward_w4_sample(x: torch.Tensor, w: W4Weights, u: torch.Tensor, temperatur
     the logits staying in the workspace."""
     sfx = _w4_input(x, w)
     M, N, K = x.shape[0], w.out_features, w.in_features
-    _need_u(u, M, x.device)
-    how = _sampling(M, x.device, temperature, top_k, top_p, min_p)
-    tokens = torch.empty(M, dtype=torch.int64, device=x.device)
-    logprobs = torch.empty(M, dtype=torch.float32, device=x.device)
+    u_ptr = _setting(u, "u", torch.float32, M, w.device)
+    how = _sampling(M, w.device, temperature, top_k, top_p, min_p)
+    tokens = torch.empty(M, dtype=torch.int64, device=w.device)
+    logprobs = torch.empty(M, dtype=torch.float32, device=w.device)
     if ws is None:
         ws = _alloc_ws(w4_sample_workspace_size(M, N, K), x.device)
     _same_device(ws, "ws", x.device)
     _call_on(w.device, "bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.ptr,
-             ctypes.byref(how), u.data_ptr(), tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel())
+             how, u_ptr, tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel())
     return tokens, logprobs
 
 

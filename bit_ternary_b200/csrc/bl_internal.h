@@ -231,17 +231,19 @@ struct SampleHow {
 cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, int64_t ld, const SampleHow& how,
                           const float* u, int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms);
 
-// Shared memory beyond 48 KB has to be allowed once per kernel and device.
+// Shared memory beyond 48 KB, and clusters of more than 8 CTAs, have to be
+// allowed once per kernel and device.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel kern, size_t bytes, std::atomic<uint64_t>& done) {
+cudaError_t allow_smem(Kernel kern, size_t bytes, std::atomic<uint64_t>& done, bool large_clusters = false) {
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
-  const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (r == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return r;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 cudaError_t launch_selftest_wait(uint32_t* err, uint64_t limit_ns, cudaStream_t stream);

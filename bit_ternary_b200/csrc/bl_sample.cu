@@ -311,18 +311,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // Another CTA's shared memory may be touched once it has begun: waited for
   // below, before the first exchange.
   cluster_arrive();
-
-  // ---- settings of the row (used after the row's loads are under way), and what
-  // later passes start from
-  const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;
-  const int kset = p.how.top_k != nullptr ? p.how.top_k[b] : p.how.top_k_value;
-  const float pset = p.how.top_p != nullptr ? p.how.top_p[b] : p.how.top_p_value;
-  const float mset = p.how.min_p != nullptr ? p.how.min_p[b] : p.how.min_p_value;
+  // What later passes start from.
   double2 tab2 = make_double2(0.0, 0.0);
   if (tid < 128) tab2 = __ldg(reinterpret_cast<const double2*>(kExp2Table.v) + tid);
   for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
   if (tid < kBins / 8) s.slice[0][tid] = s.slice[1][tid] = 0u;
   if (tid == 0) s.list_n = s.local_n = 0u;
+  // The launch may begin while the one before it runs; nothing that one may write
+  // is read, and nothing is written, before it has ended.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- settings of the row (used after the row's loads are under way)
+  const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;
+  const int kset = p.how.top_k != nullptr ? p.how.top_k[b] : p.how.top_k_value;
+  const float pset = p.how.top_p != nullptr ? p.how.top_p[b] : p.how.top_p_value;
+  const float mset = p.how.min_p != nullptr ? p.how.min_p[b] : p.how.min_p_value;
 
   // ---- the row, once: logits (NaN as -inf, -0 as 0), their extremes, how many are in
   const char* row = static_cast<const char*>(p.logits) + (b * p.ld + i0) * (kBf16 ? 2 : 4);
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       for (int j = 0; j < kLoads; ++j) {
         const int v = v0 + j * kThreads, e = v * kVec - shift;
         if (v < pieces && e >= 0 && e + kVec <= n)
-          q[j] = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)e * (kBf16 ? 2 : 4)));
+          q[j] = *reinterpret_cast<const uint4*>(row + (int64_t)e * (kBf16 ? 2 : 4));
       }
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
@@ -1097,24 +1101,22 @@ template <int kThreads, bool kBf16, bool kResident>
 cudaError_t launch_sample_t(const SampleParams& p, int64_t B, int C, size_t smem, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   auto kern = sample_kernel<kThreads, kBf16, kResident>;
-  cudaError_t e = allow_smem(kern, kSampleSmemMax, allowed);
+  const cudaError_t e = allow_smem(kern, kSampleSmemMax, allowed, true);
   if (e != cudaSuccess) return e;
-  if (C > 8) {  // more CTAs than every device has to support
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * C));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
