@@ -506,7 +506,7 @@ int bitlinear_w4_export(const void* packed, int64_t N, int64_t K, int group, int
 
 size_t bitlinear_w4_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_k(K) != BL_OK || check_mn(M, N) != BL_OK) return 0;
-  return bl::ws_w4_bytes(M, K);
+  return bl::ws_w4_bytes(M, N, K);
 }
 
 static int forward_w4_impl(const void* x, bool bf16, int64_t M, int64_t N, int64_t K, int group, int scale_type,
@@ -519,7 +519,7 @@ static int forward_w4_impl(const void* x, bool bf16, int64_t M, int64_t N, int64
   if (M == 0 || N == 0) return BL_OK;
   if (x == nullptr || packed == nullptr || y == nullptr || ws == nullptr) return BL_ERR_NULL;
   if (!aligned16(x) || !aligned16(packed) || !aligned16(y) || !aligned256(ws)) return BL_ERR_ALIGN;
-  if (ws_bytes < bl::ws_w4_bytes(M, K)) return BL_ERR_WORKSPACE;
+  if (ws_bytes < bl::ws_w4_bytes(M, N, K)) return BL_ERR_WORKSPACE;
   const int sms = num_sms_current();
   if (sms <= 0) return BL_ERR_CUDA;
   return cuda_status(
@@ -580,7 +580,7 @@ int bitlinear_sample_bf16(const uint16_t* logits, int64_t B, int64_t V, int64_t 
 
 size_t bitlinear_w4_sample_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_k(K) != BL_OK || check_mn(M, N) != BL_OK) return 0;
-  return bl::ws_w4_bytes(M, K) + bl::align256(4 * (size_t)M * (size_t)N);
+  return bl::ws_w4_bytes(M, N, K) + bl::align256(4 * (size_t)M * (size_t)N);
 }
 
 static int w4_sample_impl(const void* x, bool bf16, int64_t M, int64_t N, int64_t K, int group, int scale_type,
@@ -594,7 +594,7 @@ static int w4_sample_impl(const void* x, bool bf16, int64_t M, int64_t N, int64_
   if (M == 0) return BL_OK;
   if (ws == nullptr) return BL_ERR_NULL;
   if (ws_bytes < bitlinear_w4_sample_workspace_size(M, N, K)) return BL_ERR_WORKSPACE;
-  const size_t fwd = bl::ws_w4_bytes(M, K);
+  const size_t fwd = bl::ws_w4_bytes(M, N, K);
   float* logits = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + fwd);
   st = forward_w4_impl(x, bf16, M, N, K, group, scale_type, packed, logits, ws, fwd, stream);
   if (st != BL_OK) return st;

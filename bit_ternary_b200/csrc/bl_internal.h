@@ -208,7 +208,20 @@ __device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&pair)[4]) {
 // bf16 columns: a token of bf16 x is one, a token of fp32 x three.
 constexpr int kW4StreamCols = 16;
 bool w4_stream_fits(int64_t M, bool bf16, const W4Shape& sh);
-inline size_t ws_w4_bytes(int64_t M, int64_t K) { return kHeaderBytes + align256(6 * (size_t)M * (size_t)K); }
+// Most parts of K whose partial sums the workspace holds: none where tiles of 128
+// x 128 fill a B200's 148 SMs by themselves, or where a part's sums would not
+// start on a 16-byte boundary.
+constexpr int kW4MaxParts = 8;
+inline int w4_parts(int64_t M, int64_t N) {
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  return tiles < 148 && (M * N) % 4 == 0 ? kW4MaxParts : 1;
+}
+// [header | x as three bf16 planes | partial sums]
+inline size_t ws_w4_bytes(int64_t M, int64_t N, int64_t K) {
+  const int parts = w4_parts(M, N);
+  return kHeaderBytes + align256(6 * (size_t)M * (size_t)K) +
+         (parts > 1 ? align256(4 * (size_t)parts * (size_t)M * (size_t)N) : 0);
+}
 // The tensor-core kernel for many tokens (bl_w4_gemm.cu).
 cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, const W4Shape& sh, const uint8_t* packed, float* y,
                            void* ws, cudaStream_t stream, int num_sms);

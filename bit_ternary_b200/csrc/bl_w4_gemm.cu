@@ -3,8 +3,13 @@
 //
 //   y[m,n] = sum_G S[n,G] * (sum over k in G of c[n,k] * x[m,k])
 //
-// Tile: 128 weight rows (MMA M) x BN tokens (MMA N); a stage is 128 columns of
-// K, one block of the packed weights for each of eight row tiles.
+// Tile: H x 128 weight rows (MMA M) x BN tokens (MMA N); a stage is 128 columns
+// of K, one block of the packed weights for each of 8 H row tiles. With H = 1
+// every byte of x that TMA writes to shared memory is read by one MMA, and both
+// together take all of its bandwidth (an MMA every ~100 cycles instead of 64 for
+// 128 tokens); H = 2 uses a stage of x for two halves of the rows. Where the
+// tiles leave SMs idle, K is cut into parts: partial sums go to the workspace
+// and a second launch adds them in order.
 //   A = the codes as bf16 (c * 2^-6, exact), unpacked by four warps from
 //       registers into TMEM (tcgen05.st), a ring of stages.
 //   B = x as bf16, loaded by TMA with 128-byte swizzle: the caller's own bf16 x,
@@ -16,7 +21,7 @@
 //       tile's sums in registers. Scaling the weights instead would round them
 //       to bf16.
 // Warp roles: 0 TMA producer (TMEM owner), 1 MMA issuer, 4..7 unpack, 8..15
-// drain (a warp owns 32 rows x BN / 2 tokens). Every barrier wait is bounded in
+// drain (a warp owns 32 rows x BN / 2 tokens, or 32 rows of its half x BN). Every barrier wait is bounded in
 // time; a timeout sets a shared abort flag and the workspace's error word, and
 // all roles run out and exit.
 #include "bl_internal.h"
@@ -38,22 +43,25 @@ constexpr int kDrainWarps = 8;
 constexpr int kThreads = 32 * (kDrainWarp0 + kDrainWarps);
 constexpr size_t kSmemMax = 227 * 1024;
 
-template <int BN, int PLANES>
+template <int BN, int H, int PLANES>
 struct Shape {
-  static constexpr int kDBufs = BN == 128 ? 3 : 4;  // group accumulators in flight
-  static constexpr int kAStages = BN == 128 ? 2 : 4;
+  // Group accumulators in flight: with H = 2 one per half, drained while the other half's fills.
+  static constexpr int kDBufs = H == 2 ? 2 : (BN == 128 ? 3 : 4);
+  static constexpr int kAStages = H == 2 || BN == 128 ? 2 : 4;
   static constexpr int kACol = kDBufs * BN;
+  static constexpr int kAStageCols = H * kACols;
   static constexpr uint32_t kBoxBytes = BN * 128;   // BN tokens x 64 columns
   static constexpr uint32_t kBStageBytes = PLANES * 2 * kBoxBytes;
   static constexpr int kBStages = (int)((200 * 1024) / kBStageBytes) < 6 ? (int)((200 * 1024) / kBStageBytes) : 6;
-  static constexpr int kWarpTokens = BN / 2;
-  static_assert(kACol + kAStages * kACols <= (int)kTmemCols, "TMEM budget");
+  static constexpr int kWarpTokens = H == 2 ? BN : BN / 2;
+  static constexpr int kDrainers = kDrainWarps / H;  // warps that read an accumulator
+  static_assert(kACol + kAStages * kAStageCols <= (int)kTmemCols, "TMEM budget");
   static_assert(kBStages >= 2 && kBoxBytes % 1024 == 0, "shared memory ring");
 };
 
-template <int BN, int PLANES>
+template <int BN, int H, int PLANES>
 struct Sync {
-  using Sh = Shape<BN, PLANES>;
+  using Sh = Shape<BN, H, PLANES>;
   uint64_t full_b[Sh::kBStages];
   uint64_t empty_b[Sh::kBStages];
   uint64_t full_a[Sh::kAStages];
@@ -67,20 +75,33 @@ struct Sync {
 
 struct Params {
   const uint8_t* packed;
-  float* y;
+  float* y;           // or the partial sums [parts][M][N]
   uint32_t* err;
   int M, K;
   int64_t N;
   int64_t row_tiles;  // 16-row tiles of the packed weight
   int blocks;         // 128-column blocks per row: stages per tile
   int tiles_n;
-  int num_tiles;
+  int parts;          // of K
+  int units;          // tiles x parts
 };
 
-template <int BN, int PLANES>
+// One CTA's share: a part of a tile, stages kb .. kb_end.
+struct Unit {
+  int tile, part, kb, kb_end;
+  __device__ __forceinline__ Unit(const Params& p, int local) {
+    const int u = blockIdx.x + local * gridDim.x;
+    tile = u / p.parts;
+    part = u - tile * p.parts;
+    kb = (int)((int64_t)p.blocks * part / p.parts);
+    kb_end = (int)((int64_t)p.blocks * (part + 1) / p.parts);
+  }
+};
+
+template <int BN, int H, int PLANES>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)Shape<BN, PLANES>::kBStages * Shape<BN, PLANES>::kBStageBytes +
-         ((sizeof(Sync<BN, PLANES>) + 127) & ~size_t(127));
+  return 1024 + (size_t)Shape<BN, H, PLANES>::kBStages * Shape<BN, H, PLANES>::kBStageBytes +
+         ((sizeof(Sync<BN, H, PLANES>) + 127) & ~size_t(127));
 }
 
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, int32_t c0, int32_t c1, int32_t c2,
@@ -185,20 +206,20 @@ __device__ __forceinline__ void ring_next(int& s, uint32_t& ph) {
   }
 }
 
-template <int BN, int PLANES, int GPB, bool kBf16S>
+template <int BN, int H, int PLANES, int GPB, bool kBf16S>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const Params p) {
-  using Sh = Shape<BN, PLANES>;
+  using Sh = Shape<BN, H, PLANES>;
   constexpr int kBStages = Sh::kBStages, kAStages = Sh::kAStages, kDBufs = Sh::kDBufs, kACol = Sh::kACol;
   constexpr int kBlockBytes = kW4CodeBytes + kW4Rows * GPB * (kBf16S ? 2 : 4);
   constexpr int kSteps = kStageK / GPB / 16;  // MMAs of one group and piece
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sB = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Sync<BN, PLANES>& S = *reinterpret_cast<Sync<BN, PLANES>*>(sB + (size_t)kBStages * Sh::kBStageBytes);
+  Sync<BN, H, PLANES>& S = *reinterpret_cast<Sync<BN, H, PLANES>*>(sB + (size_t)kBStages * Sh::kBStageBytes);
 
   // Warp-uniform by construction, so that what follows from it stays in uniform registers.
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int my_tiles = p.num_tiles > (int)blockIdx.x ? (p.num_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const int my_units = p.units > (int)blockIdx.x ? (p.units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kBStages; ++s) {
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kDBufs; ++b) {
       mbar_init(&S.acc_full[b], 1);
-      mbar_init(&S.acc_empty[b], kDrainWarps);
+      mbar_init(&S.acc_empty[b], Sh::kDrainers);
     }
     mbar_init(&S.drain, 1);
     S.abort_flag = 0;
@@ -241,12 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         int issued = 0;
-        for (int lt = 0; lt < my_tiles; ++lt) {
-          const int tile = blockIdx.x + lt * gridDim.x;
-          const int m0 = (tile / p.tiles_n) * BN;
-          for (int kb = 0; kb < p.blocks; ++kb) {
+        for (int lt = 0; lt < my_units; ++lt) {
+          const Unit u(p, lt);
+          const int m0 = (u.tile / p.tiles_n) * BN;
+          for (int kb = u.kb; kb < u.kb_end; ++kb) {
             if (!mbar_wait(&S.empty_b[s], ph ^ 1, abort_flag, p.err, kDevTimeoutProducer)) {
-              lt = my_tiles;
+              lt = my_units;
               break;
             }
             // Columns past K and tokens past M arrive as zeros.
@@ -280,15 +301,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int sb = 0, sa = 0, d = 0;
       uint32_t phb = 0, pha = 0, phd = 0;
       bool ok = true, ready = false;
-      const int64_t stages = (int64_t)my_tiles * p.blocks;
+      int64_t stages = 0;
+      for (int lt = 0; lt < my_units; ++lt) {
+        const Unit u(p, lt);
+        stages += u.kb_end - u.kb;
+      }
+      constexpr int kGroups = GPB * H;  // accumulators of a stage: group by group, half by half
       for (int64_t j = 0; j < stages && ok; ++j) {
         const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (int)(Sh::kBStageBytes >> 4));
-        const uint32_t a_tmem = tmem + kACol + kACols * sa;
+        const uint32_t a_tmem = tmem + kACol + Sh::kAStageCols * sa;
         const int sa0 = sa, sb0 = sb;
 #pragma unroll
-        for (int gi = 0; gi < GPB; ++gi) {
+        for (int gh = 0; gh < kGroups; ++gh) {
+          const int gi = gh / H, h = gh % H;
           if (!ready) {
-            ok = (gi != 0 || (warp_wait(&S.full_a[sa0], pha, abort_flag, p.err, kDevTimeoutMma) &&
+            ok = (gh != 0 || (warp_wait(&S.full_a[sa0], pha, abort_flag, p.err, kDevTimeoutMma) &&
                               warp_wait(&S.full_b[sb0], phb, abort_flag, p.err, kDevTimeoutMma))) &&
                  warp_wait(&S.acc_empty[d], phd ^ 1, abort_flag, p.err, kDevTimeoutMma);
             if (!ok) break;
@@ -297,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d_tmem = tmem + d * BN;
           const int d0 = d;
           ring_next<kDBufs>(d, phd);
-          if (gi == GPB - 1) {
+          if (gh == kGroups - 1) {
             ring_next<kAStages>(sa, pha);
             ring_next<kBStages>(sb, phb);
           }
@@ -310,16 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < kSteps; ++k) {
                 if (q * kSteps + k == PLANES * kSteps - 2) {
                   seen = mbar_test(&S.acc_empty[d], phd ^ 1);
-                  if (gi == GPB - 1) seen = seen & mbar_test(&S.full_a[sa], pha) & mbar_test(&S.full_b[sb], phb);
+                  if (gh == kGroups - 1) seen = seen & mbar_test(&S.full_a[sa], pha) & mbar_test(&S.full_b[sb], phb);
                 }
                 const int ks = gi * kSteps + k;  // 16-column step of the stage
-                umma_bf16_ts(d_tmem, a_tmem + 8 * ks,
+                umma_bf16_ts(d_tmem, a_tmem + kACols * h + 8 * ks,
                              bdesc + (uint64_t)((pl * 2 + (ks >> 2)) * (int)(Sh::kBoxBytes >> 4) + 2 * (ks & 3)), idesc,
                              (q | k) != 0 ? 1u : 0u);
               }
             }
             tc_commit(&S.acc_full[d0]);
-            if (gi == GPB - 1) {
+            if (gh == kGroups - 1) {
               tc_commit(&S.empty_a[sa0]);
               tc_commit(&S.empty_b[sb0]);
             }
@@ -335,67 +362,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp < kDrainWarp0) {
-    // ------------------------------------------------ unpack: one weight row per thread
+    // ------------------------------------------------ unpack: one weight row of each half per thread
     regs_down<120>();
     if (warp == kUnpackWarp0 && lane == 0 && blockIdx.x == 0) *p.err = 0u;
     const int quarter = warp & 3;  // TMEM lane quarter (hardware rule: warp id % 4)
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    constexpr int kAhead = 3;  // stages of codes in flight
-    const int64_t stages = (int64_t)my_tiles * p.blocks;
-    uint4 buf[kAhead][4];
-    int lt = 0, kb = 0;  // the next stage to load
-    const uint8_t* src = nullptr;
-    const auto load = [&](uint4(&w)[4]) {
-      if (kb == 0) {
-        const int tile = blockIdx.x + lt * gridDim.x;
-        int64_t rt = (int64_t)(tile % p.tiles_n) * (kBM / kW4Rows) + (row / kW4Rows);
-        rt = rt < p.row_tiles ? rt : p.row_tiles - 1;  // rows past the last tile: anything in bounds
-        src = p.packed + rt * p.blocks * kBlockBytes + (row % kW4Rows) * (kStageK / 2);
+    constexpr int kAhead = H == 2 ? 2 : 3;  // stages of codes in flight
+    uint4 buf[kAhead][H][4];
+    int lt = 0, kb = 0, kb_end = 0;  // the next stage to load
+    const uint8_t* src[H];
+    const auto load = [&](uint4(&w)[H][4]) {  // false past the last stage
+      if (kb == kb_end) {
+        if (lt == my_units) return false;
+        const Unit u(p, lt++);
+        kb = u.kb;
+        kb_end = u.kb_end;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          int64_t rt = ((int64_t)(u.tile % p.tiles_n) * H + h) * (kBM / kW4Rows) + (row / kW4Rows);
+          rt = rt < p.row_tiles ? rt : p.row_tiles - 1;  // rows past the last tile: anything in bounds
+          src[h] = p.packed + (rt * p.blocks + kb) * kBlockBytes + (row % kW4Rows) * (kStageK / 2);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-      src += kBlockBytes;
-      if (++kb == p.blocks) {
-        kb = 0;
-        ++lt;
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[h][i] = *(reinterpret_cast<const uint4*>(src[h]) + i);
+        src[h] += kBlockBytes;
       }
+      ++kb;
+      return true;
     };
+    bool have[kAhead];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q)
-      if (q < stages) load(buf[q]);
+    for (int q = 0; q < kAhead; ++q) have[q] = load(buf[q]);
     int s = 0;
     uint32_t ph = 0;
-    bool ok = true;
-    for (int64_t j0 = 0; j0 < stages && ok; j0 += kAhead) {
+    for (bool ok = true; ok && have[0];) {
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
-        const int64_t j = j0 + q;
-        if (j >= stages) break;
+        if (!have[q] || !ok) break;
         if (!warp_wait(&S.empty_a[s], ph ^ 1, abort_flag, p.err, kDevTimeoutUnpack)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // Word (t, j) of the row holds columns 32 j + 8 t ..: pairs 16 j + 4 t .. of the stage.
+        // Word (t, j) of a row holds columns 32 j + 8 t ..: pairs 16 j + 4 t .. of the stage.
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
+        for (int h = 0; h < H; ++h) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t w0 = h == 0 ? buf[q][t].x : buf[q][t].z;
-            const uint32_t w1 = h == 0 ? buf[q][t].y : buf[q][t].w;
-            uint32_t pr[4];
-            w4_unpack(w0, pr);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * t + i] = pr[i];
-            w4_unpack(w1, pr);
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t w0 = c == 0 ? buf[q][h][t].x : buf[q][h][t].z;
+              const uint32_t w1 = c == 0 ? buf[q][h][t].y : buf[q][h][t].w;
+              uint32_t pr[4];
+              w4_unpack(w0, pr);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[16 + 4 * t + i] = pr[i];
+              for (int i = 0; i < 4; ++i) v[4 * t + i] = pr[i];
+              w4_unpack(w1, pr);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[16 + 4 * t + i] = pr[i];
+            }
+            tmem_st_32x32b_x32(lane_base + kACol + Sh::kAStageCols * s + kACols * h + 32 * c, v);
           }
-          tmem_st_32x32b_x32(lane_base + kACol + kACols * s + 32 * h, v);
         }
-        if (j + kAhead < stages) load(buf[q]);
+        have[q] = load(buf[q]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -404,26 +438,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------ drain: 32 rows x BN / 2 tokens per warp
+    // ------------------------------------------------ drain: 32 rows x kWarpTokens tokens per warp
     regs_up<176>();
     constexpr int kTok = Sh::kWarpTokens;
-    const int quarter = warp & 3, half = (warp - kDrainWarp0) >> 2;
+    constexpr int kChunk = kTok == 128 ? 32 : kTok;
+    const int quarter = warp & 3, half = (warp - kDrainWarp0) >> 2;  // of the tokens, or (H = 2) of the rows
     const int row = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + half * kTok;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + (H == 2 ? 0 : half * kTok);
     const int soff = kW4CodeBytes + ((row & 7) * GPB * 2 + ((row >> 3) & 1)) * (kBf16S ? 2 : 4);
-    int d = 0;
+    int d = H == 2 ? half : 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int lt = 0; lt < my_tiles && ok; ++lt) {
-      const int tile = blockIdx.x + lt * gridDim.x;
-      const int m0 = (tile / p.tiles_n) * BN + half * kTok;
-      const int64_t n = (int64_t)(tile % p.tiles_n) * kBM + row;
+    for (int lt = 0; lt < my_units && ok; ++lt) {
+      const Unit u(p, lt);
+      const int m0 = (u.tile / p.tiles_n) * BN + (H == 2 ? 0 : half * kTok);
+      const int64_t n = ((int64_t)(u.tile % p.tiles_n) * H + (H == 2 ? half : 0)) * kBM + row;
       int64_t rt = n / kW4Rows;
       rt = rt < p.row_tiles ? rt : p.row_tiles - 1;
-      const uint8_t* sp = p.packed + rt * p.blocks * kBlockBytes + soff;
+      const uint8_t* sp = p.packed + (rt * p.blocks + u.kb) * kBlockBytes + soff;
       const auto scale = [&](int gi) {
-        if (kBf16S) return bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(sp) + 2 * gi));
-        return __ldg(reinterpret_cast<const float*>(sp) + 2 * gi);
+        if (kBf16S) return bf16_bits_to_float(*(reinterpret_cast<const uint16_t*>(sp) + 2 * gi));
+        return *(reinterpret_cast<const float*>(sp) + 2 * gi);
       };
       float acc[kTok];
 #pragma unroll
@@ -431,11 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sc[GPB];
 #pragma unroll
       for (int gi = 0; gi < GPB; ++gi) sc[gi] = scale(gi);
-      for (int kb = 0; kb < p.blocks && ok; ++kb) {
+      for (int kb = u.kb; kb < u.kb_end && ok; ++kb) {
         float nsc[GPB];
         sp += kBlockBytes;
 #pragma unroll
-        for (int gi = 0; gi < GPB; ++gi) nsc[gi] = kb + 1 < p.blocks ? scale(gi) : 0.f;
+        for (int gi = 0; gi < GPB; ++gi) nsc[gi] = kb + 1 < u.kb_end ? scale(gi) : 0.f;
 #pragma unroll
         for (int gi = 0; gi < GPB; ++gi) {
           if (ok && !warp_wait(&S.acc_full[d], ph, abort_flag, p.err, kDevTimeoutEpilogue)) ok = false;
@@ -443,22 +478,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             uint64_t ss;
             asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(sc[gi]));
-            uint32_t v[kTok];
-            tmem_ld_cols(lane_base + d * BN, v);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.acc_empty[d]);  // all of it is in registers
 #pragma unroll
-            for (int i = 0; i < kTok; i += 2) fma2(acc[i], acc[i + 1], v[i], v[i + 1], ss);
-            ring_next<kDBufs>(d, ph);
+            for (int c = 0; c < kTok; c += kChunk) {
+              uint32_t v[kChunk];
+              tmem_ld_cols(lane_base + d * BN + c, v);
+              tmem_wait_ld();
+              if (c + kChunk == kTok) {  // all of it is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.acc_empty[d]);
+              }
+#pragma unroll
+              for (int i = 0; i < kChunk; i += 2) fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], ss);
+            }
+            if (H == 2) ph ^= 1;
+            else ring_next<kDBufs>(d, ph);
           }
         }
 #pragma unroll
         for (int gi = 0; gi < GPB; ++gi) sc[gi] = nsc[gi];
       }
       if (ok && n < p.N) {
-        float* out = p.y + (int64_t)m0 * p.N + n;
+        float* out = p.y + ((int64_t)u.part * p.M + m0) * p.N + n;
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
           if (m0 + i < p.M) __stcs(out, acc[i] * kW4Unit);
@@ -477,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The three bf16 pieces of an fp32 x [M, K], planes [3][M][K].
-__global__ void __launch_bounds__(256) w4_split_kernel(const float4* __restrict__ x, int64_t n4, uint2* planes) {
+__global__ void __launch_bounds__(256) w4_split_kernel(const float4* x, int64_t n4, uint2* planes) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
@@ -489,6 +530,25 @@ __global__ void __launch_bounds__(256) w4_split_kernel(const float4* __restrict_
     planes[i] = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
     planes[n4 + i] = make_uint2(m[0] | (m[1] << 16), m[2] | (m[3] << 16));
     planes[2 * n4 + i] = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+  }
+}
+
+// y = part[0] + part[1] + ..., in this order.
+__global__ void __launch_bounds__(256) w4_add_parts_kernel(const float4* part, int parts, int64_t total, float* y) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t n4 = total / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    float4 a = part[i];
+    for (int q = 1; q < parts; ++q) {
+      // total % 4 == 0 keeps every part 16-byte aligned (the launch sees to it).
+      const float4 v = part[q * n4 + i];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    reinterpret_cast<float4*>(y)[i] = a;
   }
 }
 
@@ -507,40 +567,75 @@ cudaError_t launch_dependent(Kernel kern, int grid, int threads, size_t smem, cu
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int BN, int PLANES, int GPB, bool kBf16S>
+template <int BN, int H, int PLANES, int GPB, bool kBf16S>
 cudaError_t launch_t(const CUtensorMap& tx, const Params& p, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
-  auto kern = w4_gemm_kernel<BN, PLANES, GPB, kBf16S>;
-  constexpr size_t smem = smem_bytes<BN, PLANES>();
+  auto kern = w4_gemm_kernel<BN, H, PLANES, GPB, kBf16S>;
+  constexpr size_t smem = smem_bytes<BN, H, PLANES>();
   static_assert(smem <= kSmemMax, "shared memory");
   const cudaError_t e = allow_smem(kern, smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, grid, kThreads, smem, stream, tx, p);
 }
 
-template <int BN, int PLANES>
+template <int BN, int H, int PLANES>
 cudaError_t launch_n(const CUtensorMap& tx, const Params& p, const W4Shape& sh, int grid, cudaStream_t stream) {
   const bool s16 = sh.scale_bytes == 2;
   switch (sh.group) {
-    case 32: return s16 ? launch_t<BN, PLANES, 4, true>(tx, p, grid, stream)
-                        : launch_t<BN, PLANES, 4, false>(tx, p, grid, stream);
-    case 64: return s16 ? launch_t<BN, PLANES, 2, true>(tx, p, grid, stream)
-                        : launch_t<BN, PLANES, 2, false>(tx, p, grid, stream);
-    default: return s16 ? launch_t<BN, PLANES, 1, true>(tx, p, grid, stream)
-                        : launch_t<BN, PLANES, 1, false>(tx, p, grid, stream);
+    case 32: return s16 ? launch_t<BN, H, PLANES, 4, true>(tx, p, grid, stream)
+                        : launch_t<BN, H, PLANES, 4, false>(tx, p, grid, stream);
+    case 64: return s16 ? launch_t<BN, H, PLANES, 2, true>(tx, p, grid, stream)
+                        : launch_t<BN, H, PLANES, 2, false>(tx, p, grid, stream);
+    default: return s16 ? launch_t<BN, H, PLANES, 1, true>(tx, p, grid, stream)
+                        : launch_t<BN, H, PLANES, 1, false>(tx, p, grid, stream);
   }
 }
 
-// Estimated cycles of a launch with BN-token tiles: waves of tiles times a
-// tile's stages, each as long as its MMAs, its unpacking or its drains.
-int64_t estimate(int BN, int planes, int gpb, int64_t M, int64_t tiles_n, int64_t blocks, int sms) {
-  const int64_t tiles = (M + BN - 1) / BN * tiles_n;
-  const int64_t waves = (tiles + sms - 1) / sms;
-  const int64_t mma = (int64_t)planes * 8 * (BN / 2);
-  const int64_t drain = (int64_t)gpb * (BN + 60);
+template <int PLANES>
+cudaError_t launch_p(int BN, int H, const CUtensorMap& tx, const Params& p, const W4Shape& sh, int grid,
+                     cudaStream_t stream) {
+  if (BN == 32) return launch_n<32, 1, PLANES>(tx, p, sh, grid, stream);
+  if (BN == 64) return launch_n<64, 1, PLANES>(tx, p, sh, grid, stream);
+  return H == 2 ? launch_n<128, 2, PLANES>(tx, p, sh, grid, stream) : launch_n<128, 1, PLANES>(tx, p, sh, grid, stream);
+}
+
+// How a product is cut: tokens per tile, 128-row halves, parts of K.
+struct Cut {
+  int BN, H, parts;
+};
+
+// Estimated cycles of a launch: the longest CTA's units, each stage of them as
+// long as its MMAs, its unpacking or its drains, whichever takes longest
+// (cycles per stage measured on 4096, 1024 and 512 tokens), and for parts the
+// second launch and its traffic.
+int64_t estimate(const Cut& c, int planes, int gpb, int64_t M, int64_t N, int64_t blocks, int sms) {
+  const int64_t tiles = (M + c.BN - 1) / c.BN * ((N + kBM * c.H - 1) / (kBM * c.H));
+  const int64_t waves = (tiles * c.parts + sms - 1) / sms;
+  const int64_t per_mma = c.BN == 128 ? (c.H == 2 ? 75 : 100) : (c.BN == 64 ? 55 : 50);
+  const int64_t mma = (int64_t)planes * 8 * c.H * per_mma;
+  const int64_t drain = (int64_t)gpb * (c.H == 2 ? 2 * 300 : (c.BN == 128 ? 400 : 300));
+  const int64_t unpack = 300 * c.H;
   int64_t stage = mma > drain ? mma : drain;
-  stage = stage > 260 ? stage : 260;
-  return waves * (blocks * stage + 1500);
+  stage = stage > unpack ? stage : unpack;
+  const int64_t add = c.parts > 1 ? 5000 + M * N * c.parts / sms / 8 : 0;
+  return waves * ((blocks + c.parts - 1) / c.parts * stage + 2000 * c.H) + add;
+}
+
+Cut choose_cut(int planes, int gpb, int64_t M, int64_t N, int64_t blocks, int sms) {
+  Cut best{32, 1, 1};
+  int64_t cost = estimate(best, planes, gpb, M, N, blocks, sms);
+  const int most = w4_parts(M, N);
+  for (const Cut shape : {Cut{32, 1, 1}, Cut{64, 1, 1}, Cut{128, 1, 1}, Cut{128, 2, 1}}) {
+    for (int parts = 1; parts <= most && parts <= blocks; ++parts) {
+      const Cut c{shape.BN, shape.H, parts};
+      const int64_t e = estimate(c, planes, gpb, M, N, blocks, sms);
+      if (e < cost) {
+        cost = e;
+        best = c;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -570,17 +665,16 @@ cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, const W4Shape& s
   p.N = sh.N;
   p.row_tiles = sh.tiles();
   p.blocks = (int)sh.blocks();
-  const int64_t tiles_n = (sh.N + kBM - 1) / kBM;
+  const Cut c = choose_cut(planes, kW4Cols / sh.group, M, sh.N, p.blocks, num_sms);
+  const int BN = c.BN;
+  const int64_t tiles_n = (sh.N + kBM * c.H - 1) / (kBM * c.H);
   p.tiles_n = (int)tiles_n;
-  const int gpb = kW4Cols / sh.group;
-  int BN = 32;
-  for (const int cand : {64, 128})
-    if (estimate(cand, planes, gpb, M, tiles_n, p.blocks, num_sms) <
-        estimate(BN, planes, gpb, M, tiles_n, p.blocks, num_sms))
-      BN = cand;
-  const int64_t nt = (M + BN - 1) / BN * tiles_n;
+  p.parts = c.parts;
+  const int64_t nt = (M + BN - 1) / BN * tiles_n * c.parts;
   if (nt > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  p.num_tiles = (int)nt;
+  p.units = (int)nt;
+  float* parts = reinterpret_cast<float*>(base + kHeaderBytes + align256(6 * (size_t)M * (size_t)sh.K));
+  if (c.parts > 1) p.y = parts;
   CUtensorMap tx;
   const cuuint64_t gdim[3] = {(cuuint64_t)sh.K, (cuuint64_t)M, (cuuint64_t)planes};
   const cuuint64_t gstride[2] = {(cuuint64_t)sh.K * 2, (cuuint64_t)sh.K * 2 * (cuuint64_t)M};
@@ -591,12 +685,12 @@ cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, const W4Shape& s
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const int grid = (int)(nt < num_sms ? nt : num_sms);
-  if (planes == 1) {
-    if (BN == 32) return launch_n<32, 1>(tx, p, sh, grid, stream);
-    return BN == 64 ? launch_n<64, 1>(tx, p, sh, grid, stream) : launch_n<128, 1>(tx, p, sh, grid, stream);
-  }
-  if (BN == 32) return launch_n<32, 3>(tx, p, sh, grid, stream);
-  return BN == 64 ? launch_n<64, 3>(tx, p, sh, grid, stream) : launch_n<128, 3>(tx, p, sh, grid, stream);
+  const cudaError_t e = planes == 1 ? launch_p<1>(BN, c.H, tx, p, sh, grid, stream)
+                                    : launch_p<3>(BN, c.H, tx, p, sh, grid, stream);
+  if (e != cudaSuccess || c.parts == 1) return e;
+  const int64_t total = M * sh.N, want = (total / 4 + 255) / 256, most = (int64_t)num_sms * 8;
+  return launch_dependent(w4_add_parts_kernel, (int)(want < most ? want : most), 256, 0, stream,
+                          static_cast<const float4*>(static_cast<const void*>(parts)), c.parts, total, y);
 }
 
 }  // namespace bl
