@@ -46,8 +46,8 @@ constexpr size_t kSmemMax = 227 * 1024;
 template <int BN, int H, int PLANES>
 struct Shape {
   // Group accumulators in flight: with H = 2 one per half, drained while the other half's fills.
-  static constexpr int kDBufs = H == 2 ? 2 : (BN == 128 ? 3 : 4);
-  static constexpr int kAStages = H == 2 || BN == 128 ? 2 : 4;
+  static constexpr int kDBufs = H == 2 || BN == 128 ? 2 : 4;
+  static constexpr int kAStages = H == 2 ? 2 : 4;
   static constexpr int kACol = kDBufs * BN;
   static constexpr int kAStageCols = H * kACols;
   static constexpr uint32_t kBoxBytes = BN * 128;   // BN tokens x 64 columns
@@ -62,6 +62,7 @@ struct Shape {
 template <int BN, int H, int PLANES>
 struct Sync {
   using Sh = Shape<BN, H, PLANES>;
+  // Each empty_x right after its full_x (the MMA issuer counts on it).
   uint64_t full_b[Sh::kBStages];
   uint64_t empty_b[Sh::kBStages];
   uint64_t full_a[Sh::kAStages];
@@ -187,6 +188,21 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tc_commit_at(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -289,70 +305,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------ MMA issuer
-      // The whole warp walks the groups and one lane issues: addresses and
-      // descriptors stay in uniform registers, as the instruction wants them. A
-      // lane of its own (a divergent branch) needed 135 cycles an MMA for the
-      // moves, where 128 tokens take the tensor pipe 64. The barriers of the next
-      // group are looked at before the last MMAs of this one are issued: waiting
-      // for them in turn took 450 cycles a stage, which the pipe's queue (a few
-      // MMAs) does not cover.
+      // The whole warp walks the groups and one lane issues, so that descriptors
+      // and addresses stay in uniform registers, as the instruction wants them
+      // (a lane of its own, in a divergent branch, needed 135 cycles an MMA for
+      // the moves, where 128 tokens take the tensor pipe 64). The pipe's queue
+      // covers a few MMAs, and beside busy warps every instruction between two
+      // groups costs this warp some eight cycles: barriers are 32-bit addresses
+      // counted up, all of a group's are tried at once, and stages are counted in
+      // 32 bits.
       const uint32_t idesc = umma_idesc_bf16(kBM, BN);
       const uint64_t bdesc0 = umma_sdesc_sw128(sB);
-      int sb = 0, sa = 0, d = 0;
-      uint32_t phb = 0, pha = 0, phd = 0;
-      bool ok = true, ready = false;
-      int64_t stages = 0;
+      const uint32_t bhi = (uint32_t)(bdesc0 >> 32), blo0 = (uint32_t)bdesc0;
+      const uint32_t a0 = smem_u32(&S.full_a[0]), b0 = smem_u32(&S.full_b[0]), d0 = smem_u32(&S.acc_full[0]);
+      constexpr uint32_t kAEmpty = kAStages * 8, kBEmpty = kBStages * 8, kDEmpty = kDBufs * 8;  // empty_x follows full_x
+      uint32_t sb = 0, sa = 0, d = 0;
+      uint32_t phb = 0, pha = 0, phd = 1;
+      bool ok = true;
+      uint32_t stages = 0;
       for (int lt = 0; lt < my_units; ++lt) {
         const Unit u(p, lt);
         stages += u.kb_end - u.kb;
       }
       constexpr int kGroups = GPB * H;  // accumulators of a stage: group by group, half by half
-      for (int64_t j = 0; j < stages && ok; ++j) {
-        const uint64_t bdesc = bdesc0 + (uint64_t)(sb * (int)(Sh::kBStageBytes >> 4));
+      for (uint32_t j = 0; j < stages && ok; ++j) {
+        const uint32_t blo = blo0 + sb * (Sh::kBStageBytes >> 4);
         const uint32_t a_tmem = tmem + kACol + Sh::kAStageCols * sa;
-        const int sa0 = sa, sb0 = sb;
 #pragma unroll
         for (int gh = 0; gh < kGroups; ++gh) {
           const int gi = gh / H, h = gh % H;
-          if (!ready) {
-            ok = (gh != 0 || (warp_wait(&S.full_a[sa0], pha, abort_flag, p.err, kDevTimeoutMma) &&
-                              warp_wait(&S.full_b[sb0], phb, abort_flag, p.err, kDevTimeoutMma))) &&
-                 warp_wait(&S.acc_empty[d], phd ^ 1, abort_flag, p.err, kDevTimeoutMma);
+          bool there = mbar_try_wait_at(d0 + kDEmpty + 8 * d, phd);
+          if (gh == 0) there = there & mbar_try_wait_at(a0 + 8 * sa, pha) & mbar_try_wait_at(b0 + 8 * sb, phb);
+          if (!__all_sync(0xFFFFFFFFu, there)) {
+            ok = (gh != 0 || (warp_wait(&S.full_a[sa], pha, abort_flag, p.err, kDevTimeoutMma) &&
+                              warp_wait(&S.full_b[sb], phb, abort_flag, p.err, kDevTimeoutMma))) &&
+                 warp_wait(&S.acc_empty[d], phd, abort_flag, p.err, kDevTimeoutMma);
             if (!ok) break;
           }
           tc_fence_after();
-          const uint32_t d_tmem = tmem + d * BN;
-          const int d0 = d;
-          ring_next<kDBufs>(d, phd);
-          if (gh == kGroups - 1) {
-            ring_next<kAStages>(sa, pha);
-            ring_next<kBStages>(sb, phb);
-          }
-          bool seen = false;
           if (elect_one()) {
+            const uint32_t d_tmem = tmem + d * BN;
 #pragma unroll
             for (int q = 0; q < PLANES; ++q) {
               const int pl = PLANES - 1 - q;  // the smallest piece first
 #pragma unroll
               for (int k = 0; k < kSteps; ++k) {
-                if (q * kSteps + k == PLANES * kSteps - 2) {
-                  seen = mbar_test(&S.acc_empty[d], phd ^ 1);
-                  if (gh == kGroups - 1) seen = seen & mbar_test(&S.full_a[sa], pha) & mbar_test(&S.full_b[sb], phb);
-                }
                 const int ks = gi * kSteps + k;  // 16-column step of the stage
-                umma_bf16_ts(d_tmem, a_tmem + kACols * h + 8 * ks,
-                             bdesc + (uint64_t)((pl * 2 + (ks >> 2)) * (int)(Sh::kBoxBytes >> 4) + 2 * (ks & 3)), idesc,
+                const uint32_t lo = blo + (pl * 2 + (ks >> 2)) * (Sh::kBoxBytes >> 4) + 2 * (ks & 3);
+                umma_bf16_ts(d_tmem, a_tmem + kACols * h + 8 * ks, ((uint64_t)bhi << 32) | lo, idesc,
                              (q | k) != 0 ? 1u : 0u);
               }
             }
-            tc_commit(&S.acc_full[d0]);
+            tc_commit_at(d0 + 8 * d);
             if (gh == kGroups - 1) {
-              tc_commit(&S.empty_a[sa0]);
-              tc_commit(&S.empty_b[sb0]);
+              tc_commit_at(a0 + kAEmpty + 8 * sa);
+              tc_commit_at(b0 + kBEmpty + 8 * sb);
             }
           }
-          ready = __any_sync(0xFFFFFFFFu, seen);
+          __syncwarp();
+          d = d + 1 == kDBufs ? 0 : d + 1;
+          phd ^= d == 0 ? 1u : 0u;
         }
+        sa = sa + 1 == kAStages ? 0 : sa + 1;
+        pha ^= sa == 0 ? 1u : 0u;
+        sb = sb + 1 == kBStages ? 0 : sb + 1;
+        phb ^= sb == 0 ? 1u : 0u;
       }
       // All issued MMAs complete before TMEM is released.
       if (elect_one()) {
@@ -456,28 +472,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t rt = n / kW4Rows;
       rt = rt < p.row_tiles ? rt : p.row_tiles - 1;
       const uint8_t* sp = p.packed + (rt * p.blocks + u.kb) * kBlockBytes + soff;
-      const auto scale = [&](int gi) {
-        if (kBf16S) return bf16_bits_to_float(*(reinterpret_cast<const uint16_t*>(sp) + 2 * gi));
-        return *(reinterpret_cast<const float*>(sp) + 2 * gi);
+      // Bits as loaded: a conversion here would wait for the load (500 cycles a
+      // stage), where it is only used a stage later.
+      const auto scale_bits = [&](int gi) -> uint32_t {
+        if (kBf16S) return *(reinterpret_cast<const uint16_t*>(sp) + 2 * gi);
+        return *(reinterpret_cast<const uint32_t*>(sp) + 2 * gi);
       };
       float acc[kTok];
 #pragma unroll
       for (int i = 0; i < kTok; ++i) acc[i] = 0.f;
-      float sc[GPB];
+      uint32_t sc[GPB];
 #pragma unroll
-      for (int gi = 0; gi < GPB; ++gi) sc[gi] = scale(gi);
+      for (int gi = 0; gi < GPB; ++gi) sc[gi] = scale_bits(gi);
       for (int kb = u.kb; kb < u.kb_end && ok; ++kb) {
-        float nsc[GPB];
+        uint32_t nsc[GPB] = {};
         sp += kBlockBytes;
+        if (kb + 1 < u.kb_end) {
 #pragma unroll
-        for (int gi = 0; gi < GPB; ++gi) nsc[gi] = kb + 1 < u.kb_end ? scale(gi) : 0.f;
+          for (int gi = 0; gi < GPB; ++gi) nsc[gi] = scale_bits(gi);
+        }
 #pragma unroll
         for (int gi = 0; gi < GPB; ++gi) {
           if (ok && !warp_wait(&S.acc_full[d], ph, abort_flag, p.err, kDevTimeoutEpilogue)) ok = false;
           if (ok) {
             tc_fence_after();
             uint64_t ss;
-            asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(sc[gi]));
+            asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(kBf16S ? sc[gi] << 16 : sc[gi]));
 #pragma unroll
             for (int c = 0; c < kTok; c += kChunk) {
               uint32_t v[kChunk];
