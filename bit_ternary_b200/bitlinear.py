@@ -334,14 +334,21 @@ class W4Weights:
         _need_cuda(data, "data", torch.uint8)
         if data.numel() != need:
             raise ValueError(f"data must hold {need} bytes")
-        self.data = data
+        self._data = data
         self.out_features = N
         self.in_features = K
         self.group = group
         self.scale_dtype = scale_dtype
         self.scale_type = _W4_SCALES[scale_dtype]
-        self.device = data.device
-        self.ptr = data.data_ptr()
+
+    @property
+    def data(self) -> torch.Tensor:
+        """The packed bytes (another tensor needs another W4Weights, which checks it)."""
+        return self._data
+
+    @property
+    def device(self) -> torch.device:
+        return self._data.device
 
 
 def _w4_packed_bytes(N: int, K: int, group: int, scale_dtype: torch.dtype) -> int:
@@ -395,9 +402,9 @@ def import_w4(codes: torch.Tensor, S: torch.Tensor, group: int) -> W4Weights:
 def unpack_w4(w: W4Weights) -> Tuple[torch.Tensor, torch.Tensor]:
     """The codes (int8 [N, K], -8 .. 7) and scales [N, ceil(K/group)] of a packed weight."""
     N, K = w.out_features, w.in_features
-    codes = torch.empty((N, K), dtype=torch.int8, device=w.data.device)
-    S = torch.empty((N, -(-K // w.group)), dtype=w.scale_dtype, device=w.data.device)
-    _call_on(w.device, "bitlinear_w4_export", w.ptr, N, K, w.group, w.scale_type, codes.data_ptr(), S.data_ptr())
+    codes = torch.empty((N, K), dtype=torch.int8, device=w.device)
+    S = torch.empty((N, -(-K // w.group)), dtype=w.scale_dtype, device=w.device)
+    _call_on(w.device, "bitlinear_w4_export", w._data.data_ptr(), N, K, w.group, w.scale_type, codes.data_ptr(), S.data_ptr())
     return codes, S
 
 
@@ -424,20 +431,21 @@ def forward_w4(x: torch.Tensor, w: W4Weights, out: Optional[torch.Tensor] = None
     bf16 (not quantised), y fp32. Calls that can overlap need a workspace each."""
     sfx = _w4_input(x, w)
     M, N, K = x.shape[0], w.out_features, w.in_features
+    device = w.device
     if out is None:
-        y = torch.empty(M, N, dtype=torch.float32, device=w.device)
+        y = torch.empty(M, N, dtype=torch.float32, device=device)
     else:
         y = out
         _need_cuda(y, "out", torch.float32)
-        _same_device(y, "out", w.device)
+        _same_device(y, "out", device)
         if tuple(y.shape) != (M, N):
             raise ValueError(f"out must have shape [{M}, {N}], got {list(y.shape)}")
     if ws is None:
-        ws = _alloc_ws(w4_workspace_size(M, N, K), w.device)
+        ws = _alloc_ws(w4_workspace_size(M, N, K), device)
     else:
-        _same_device(ws, "ws", w.device)
-    _call_on(w.device, "bitlinear_forward_w4" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.ptr,
-             y.data_ptr(), ws.data_ptr(), ws.numel())
+        _same_device(ws, "ws", device)
+    _call_on(device, "bitlinear_forward_w4" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type,
+             w._data.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
@@ -458,7 +466,8 @@ def _sampling(B: int, device: torch.device, temperature, top_k, top_p, min_p) ->
     if isinstance(top_k, torch.Tensor):
         how.top_k = _setting(top_k, "top_k", torch.int32, B, device)
     else:
-        how.top_k_value = top_k
+        # Past int32 it is off (V <= 2^22); ctypes would take it modulo 2^32.
+        how.top_k_value = top_k if -(1 << 31) <= top_k < 1 << 31 else 0
     if isinstance(top_p, torch.Tensor):
         how.top_p = _setting(top_p, "top_p", torch.float32, B, device)
     else:
@@ -505,15 +514,16 @@ def forward_w4_sample(x: torch.Tensor, w: W4Weights, u: torch.Tensor, temperatur
     the logits staying in the workspace."""
     sfx = _w4_input(x, w)
     M, N, K = x.shape[0], w.out_features, w.in_features
-    u_ptr = _setting(u, "u", torch.float32, M, w.device)
-    how = _sampling(M, w.device, temperature, top_k, top_p, min_p)
-    tokens = torch.empty(M, dtype=torch.int64, device=w.device)
-    logprobs = torch.empty(M, dtype=torch.float32, device=w.device)
+    device = w.device
+    u_ptr = _setting(u, "u", torch.float32, M, device)
+    how = _sampling(M, device, temperature, top_k, top_p, min_p)
+    tokens = torch.empty(M, dtype=torch.int64, device=device)
+    logprobs = torch.empty(M, dtype=torch.float32, device=device)
     if ws is None:
-        ws = _alloc_ws(w4_sample_workspace_size(M, N, K), x.device)
-    _same_device(ws, "ws", x.device)
-    _call_on(w.device, "bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type, w.ptr,
-             how, u_ptr, tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel())
+        ws = _alloc_ws(w4_sample_workspace_size(M, N, K), device)
+    _same_device(ws, "ws", device)
+    _call_on(device, "bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type,
+             w._data.data_ptr(), how, u_ptr, tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel())
     return tokens, logprobs
 
 

@@ -14,6 +14,13 @@
 // exponential. The tokens of those bins (some hundreds) are sorted and settle
 // the border exactly. Top-p then needs one exponential per token for the exact
 // sum, a draw without filters likewise, top-k none beyond the kept tokens.
+//
+// Few rows are bound by the chain of barriers (one over a cluster takes about
+// 1 us), so a row is spread over up to 16 CTAs and no CTA waits for another's
+// verdict; many rows by instructions (under top-p a token takes an exponential in
+// fp64, an atomic and its places), not by the single read of the logits.
+// Measured, fp32 logits: 1 x 128000, top-k and top-p, 17 us; 32 x 32000 without
+// filters 11 us; 256 x 128000 with top-p 317 us (131 MB: a copy's rate is 20 us).
 #include "bl_internal.h"
 
 #include <cstddef>
@@ -101,8 +108,10 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();
 }
+
 struct Sums {
-  u64 a, b, c;
+  u64 a, b;  // of every thread
+  u64 c;     // of every CTA: the same value in its threads
 };
 
 // What follows from a histogram.
@@ -319,8 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   if (tid == 0) s.list_n = s.local_n = 0u;
   // The launch may begin while the one before it runs; nothing that one may write
   // is read, and nothing is written, before it has ended.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Only now may the next launch begin: whatever it does before its own wait, the
+  // work before this one is behind it.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- settings of the row (used after the row's loads are under way)
   const float T = p.how.temperature != nullptr ? p.how.temperature[b] : p.how.temperature_value;

@@ -256,6 +256,67 @@ def test_decode_step_end_to_end(B, M, bf16):
     assert torch.equal(greedy, logits.argmax(1))
 
 
+def test_a_batch_of_many_short_rows(B):
+    rows, V = 100003, 3
+    x, u = body(rows, V, 16)
+    tok, _ = B.sample(put(x), torch.from_numpy(u).cuda(), 0.9, 2)
+    tok = tok.cpu().numpy()
+    for r in list(range(0, rows, 997)) + [rows - 1]:
+        assert tok[r] == SO.sample_row(x[r], float(u[r]), float(np.float32(0.9)), 2, 1.0, 0.0)[0]
+
+
+def test_settings_past_their_types(B):
+    """A top_k that no int32 holds filters nothing, and a negative one neither."""
+    x, u = body(2, 5000, 17)
+    xd, ud = put(x), torch.from_numpy(u).cuda()
+    ref = B.sample(xd, ud)[0]
+    for k in (1 << 31, (1 << 32) + 1, -(1 << 31), 1 - (1 << 32), 5000, 4999 + (1 << 33)):
+        assert torch.equal(B.sample(xd, ud, top_k=k)[0], ref), k
+    with pytest.raises(TypeError):
+        B.sample(xd, ud, top_k=1.5)
+    # A temperature that fp32 rounds to zero or to infinity.
+    assert torch.equal(B.sample(xd, ud, 1e-60)[0], xd.argmax(1))
+    check(B, xd, u, T=float("inf"))
+
+
+@pytest.mark.parametrize("M", [1, 24])
+def test_decode_loop_in_a_graph(B, M):
+    """Steps that feed one another, captured as one graph: launches that begin while
+    the one before them runs read what it writes. Equal to steps taken one by one."""
+    K, N, steps = 256, 2003, 6
+    g = np.random.default_rng([18, M])
+    w = B.pack_weights_w4(put((g.standard_normal((N, K)) * 0.3).astype(np.float32)), 32)
+    embedding = put(g.standard_normal((N, K)).astype(np.float32))
+    start, u = torch.zeros(M, dtype=torch.int64, device="cuda"), torch.zeros(steps, M, device="cuda")
+    ws = torch.empty(B.w4_sample_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
+
+    def loop(sync):
+        tok, out = start, []
+        for i in range(steps):
+            x = embedding[tok]
+            tok, lp = B.forward_w4_sample(x, w, u[i], 0.9, 100, 0.95, ws=ws)
+            logits = B.forward_w4(x, w, ws=ws)  # into the same workspace
+            tok, lp = B.sample(logits, u[i], 0.9, 100, 0.95)
+            out += [tok, lp]
+            if sync:
+                torch.cuda.synchronize()
+        return torch.stack([t.double() for t in out])
+
+    loop(True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = loop(False)
+    for seed in (1, 2):
+        r = np.random.default_rng([19, M, seed])
+        start.copy_(torch.from_numpy(r.integers(0, N, M)))
+        u.copy_(torch.from_numpy(r.random((steps, M)).astype(np.float32)))
+        ref = loop(True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+        assert torch.equal(loop(False), ref)
+
+
 def test_refusals(B):
     x, u = put(np.zeros((2, 8), np.float32)), torch.zeros(2, device="cuda")
     with pytest.raises(ValueError):

@@ -259,6 +259,38 @@ def test_offsets_past_32_bits(B):
             check(y[:, rows], x, c, S[rows].cpu().numpy(), group)
 
 
+@pytest.mark.parametrize("M", [2, 90, 300])
+def test_two_calls_at_once(B, M):
+    """Calls of one weight on two streams, a workspace each."""
+    N, K = 900, 640
+    codes, S = make(N, K, 64, True, 31)
+    w = put(B, codes, S, 64, True)
+    xs = [make_x(M, K, False, 32 + i) for i in range(2)]
+    xd = [put_x(x, False) for x in xs]
+    ws = [torch.empty(B.w4_workspace_size(M, N, K), dtype=torch.uint8, device="cuda") for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    ys = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                ys[i].append(B.forward_w4(xd[i], w, ws=ws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        check(ys[i][0], xs[i], codes, S, 64)
+        assert all(torch.equal(y, ys[i][0]) for y in ys[i])
+
+
+def test_packed_bytes_stay_with_their_weight(B):
+    codes, S = make(32, 64, 32, False, 33)
+    w = put(B, codes, S, 32, False)
+    with pytest.raises(AttributeError):
+        w.data = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    v = B.W4Weights(w.data.clone(), 32, 64, 32, torch.float32)
+    x = put_x(make_x(3, 64, False, 34), False)
+    assert torch.equal(B.forward_w4(x, v), B.forward_w4(x, w))
+
+
 def test_refusals(B):
     codes, S = make(32, 64, 32, False, 30)
     w = put(B, codes, S, 32, False)
