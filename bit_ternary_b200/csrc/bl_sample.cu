@@ -11,8 +11,8 @@
 // per token: a count and the sum of the tokens' places in the bin. Counts place
 // the k-th token in a bin exactly; the places bound every bin's weight to
 // about 0.05%, which places the border of top-p within a bin or two without an
-// exponential. The tokens of those bins (some hundreds) are sorted and settle
-// the border exactly. Top-p then needs one exponential per token for the exact
+// exponential. The tokens of those bins (some hundreds) settle the
+// border exactly. Top-p then needs one exponential per token for the exact
 // sum, a draw without filters likewise, top-k none beyond the kept tokens.
 //
 // Few rows are bound by the chain of barriers (one over a cluster takes about
@@ -32,6 +32,7 @@ namespace {
 constexpr int kMaxWarps = 32;
 constexpr int kBins = 2048;          // the last one holds what lies past the range
 constexpr int kListMax = 1024;       // tokens that a list of candidates holds
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;  // of a key, where a border is sought among candidates
 constexpr int kWholeMax = 512;       // up to this many the draw itself runs from the list (a sort in registers)
 constexpr int kMaxCluster = 16;
 constexpr int kPackMax = 16383;      // tokens per CTA whose count and places fit 14 + 18 bits
@@ -62,6 +63,8 @@ struct alignas(16) Smem {
     uint32_t hist[kBins];    // this CTA's histogram: counts above sums of places
     u64 local[kListMax];     // this CTA's candidates
     u64 wlist[kListMax];     // weights of the list
+    uint32_t part[2 * kMaxWarps * 32];  // weights by the thread that owns the token, likewise
+    uint32_t digit[2 * kDigits];  // weights by a digit of the key: low 20 bits, the others
   };
   alignas(16) double tab[256];           // 2^(40 + j / 256)
   alignas(16) u64 red[3][kMaxWarps];
@@ -73,11 +76,9 @@ struct alignas(16) Smem {
   int bin_lo, bin_hi;        // bins of the candidates
   uint32_t mode;
   uint32_t lo_key, hi_key;   // their keys: lo_key <= key < hi_key
-  uint32_t cut;              // kept: key > cut, and the first `ties` with key == cut
-  uint32_t cut_partial;      // more tokens than `ties` have that key
-  alignas(16) u64 ties, need, count;
+  alignas(16) u64 need, count;
 };
-static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, xch) % 16 == 0 && offsetof(Smem, ties) % 16 == 0, "alignment");
+static_assert(sizeof(Smem) % 16 == 0 && offsetof(Smem, xch) % 16 == 0 && offsetof(Smem, need) % 16 == 0, "alignment");
 
 // Shared memory of another CTA of the cluster, by its address there.
 __device__ __forceinline__ uint32_t remote_addr(const void* mine, int rank) {
@@ -668,41 +669,76 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
   };
   // From a list of the m tokens of consecutive bins: the border after the
-  // shortest run, largest first, of `need` tokens, or of weight `need`. Every CTA
-  // has the list and comes to the same border.
+  // shortest run, largest first, of `need` tokens, or of weight `need`, which the
+  // list holds. Every CTA has the list and comes to the same border. Digits of the
+  // key from the top, kDigits values each: weights added up per value, the value
+  // that holds the border, then its keys alone (two rounds for most rows; a sort of
+  // 800 candidates in all CTAs took a quarter of a row's time, 21000 of 85000 cycles).
   const auto settle = [&](int m, u64 need, bool by_weight) {
-    block_sort<kThreads>(s.list, m, true);
     constexpr int kE = kListMax / kThreads;
-    u64 w[kE], sum = 0, all;
+    uint32_t key[kE];
+    u64 w[kE];
+    uint32_t hk = 0u, lk = 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < kE; ++j) {
-      const int i = tid * kE + j;
-      w[j] = i < m ? (by_weight ? key_weight((uint32_t)(s.list[i] >> 32), r, s.tab) : 1ull) : 0ull;
-      sum += w[j];
-    }
-    u64 run = block_scan<kThreads>(sum, s, all);
-#pragma unroll
-    for (int j = 0; j < kE; ++j) {
-      const int i = tid * kE + j;
-      if (i < m && run < need && run + w[j] >= need) {
-        const uint32_t key = (uint32_t)(s.list[i] >> 32);
-        int lo = 0, hi = i;  // the first token of this key
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if ((uint32_t)(s.list[mid] >> 32) > key) lo = mid + 1;
-          else hi = mid;
-        }
-        s.cut = key;
-        s.ties = (u64)(i - lo + 1);
-        s.cut_partial = i + 1 < m && (uint32_t)(s.list[i + 1] >> 32) == key ? 1u : 0u;
+      const int i = tid + j * kThreads;
+      key[j] = i < m ? (uint32_t)(s.list[i] >> 32) : 0u;
+      w[j] = i < m ? (by_weight ? key_weight(key[j], r, s.tab) : 1ull) : 0ull;
+      if (i < m) {
+        hk = max(hk, key[j]);
+        lk = min(lk, key[j]);
       }
-      run += w[j];
     }
+    hk = __reduce_max_sync(0xFFFFFFFFu, hk);
+    lk = __reduce_min_sync(0xFFFFFFFFu, lk);
+    if (lane == 0) s.red[1][wid] = ((u64)hk << 32) | lk;
+    __syncthreads();
+    {
+      const u64 v = lane < kWarps ? s.red[1][lane] : 0xFFFFFFFFull;
+      hk = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(v >> 32));
+      lk = __reduce_min_sync(0xFFFFFFFFu, (uint32_t)v);
+    }
+    for (int round = 0; round < (32 + kDigitBits - 1) / kDigitBits; ++round) {
+      const int width = 32 - __clz(hk - lk);  // bits that differ
+      const int sh = width > kDigitBits ? width - kDigitBits : 0;
+      for (int i = tid; i < 2 * kDigits; i += kThreads) s.digit[i] = 0u;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kE; ++j) {
+        if (w[j] != 0ull && key[j] >= lk && key[j] <= hk) {
+          // 1024 weights of up to 2^40, in two words of 20 bits and the rest.
+          const uint32_t d = (hk - key[j]) >> sh;
+          if (by_weight) {
+            atomicAdd(&s.digit[d], (uint32_t)w[j] & 0xFFFFFu);
+            atomicAdd(&s.digit[kDigits + d], (uint32_t)(w[j] >> 20));
+          } else {
+            atomicAdd(&s.digit[d], 1u);
+          }
+        }
+      }
+      __syncthreads();
+      const u64 mine = tid < kDigits ? s.digit[tid] + ((u64)s.digit[kDigits + tid] << 20) : 0ull;
+      u64 all;
+      const u64 run = block_scan<kThreads>(mine, s, all);
+      if (run < need && run + mine >= need) {
+        const uint32_t top = hk - ((uint32_t)tid << sh), span = (1u << sh) - 1u;
+        s.hi_key = top;
+        s.lo_key = top - lk > span ? top - span : lk;
+        s.need = need - run;
+        s.count = mine;  // weight of the value's tokens
+      }
+      __syncthreads();
+      hk = s.hi_key;
+      lk = s.lo_key;
+      need = s.need;
+      if (sh == 0) break;
+    }
+    const u64 each = by_weight ? key_weight(hk, r, s.tab) : 1ull, weight_all = s.count;
     __syncthreads();
     if (tid == 0) s.list_n = s.local_n = 0u;
-    cut = key_value(s.cut);
-    ties = s.ties;
-    partial = s.cut_partial != 0u;
+    cut = key_value(hk);
+    ties = (need + each - 1) / each;
+    partial = ties * each < weight_all;
     __syncthreads();
   };
   // The border without a list (more equal or near tokens than one holds):
@@ -975,6 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   const int t0 = own * tid < n ? own * tid : n, t1 = t0 + own < n ? t0 + own : n;
   u64 sure = 0;           // weight of the thread's tokens that are kept whatever the border
   uint32_t sure_to = 0u;  // those at places before this one
+  int listed = 0;         // the kept tokens at other places are among this many in the list
 
   // ---- top-p
   if (by_p) {
@@ -1044,6 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
     if (mode == kBorder) {
       settle((int)v.c, need - v.b, true);
+      if (!partial) listed = (int)v.c;
     } else {
       bin_range(whole, 1u, 0xFFFFFFFFu);
       if (!zoom(need - v.b, true, s.lo_key, s.hi_key, count)) {
@@ -1071,12 +1109,31 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     return w >= wmin ? w : 0ull;
   };
   u64 sum = sure, tr = tie;
+  if (listed != 0) {
+    // To the threads that own them, in two words as above; a pass over all tokens
+    // took a tenth of a row's time.
+    for (int i = tid; i < 2 * kThreads; i += kThreads) s.part[i] = 0u;
+    __syncthreads();
+    const uint32_t cut_key = sample_key(cut);
+    for (int i = tid; i < listed; i += kThreads) {
+      const u64 e = s.list[i];
+      const int at_i = (int)((int64_t)(0xFFFFFFFFu - (uint32_t)e) - i0);
+      if ((uint32_t)(e >> 32) < cut_key || at_i < 0 || at_i >= n) continue;
+      const u64 w = key_weight((uint32_t)(e >> 32), r, s.tab);
+      if (w < wmin) continue;
+      atomicAdd(&s.part[at_i / own], (uint32_t)w & 0xFFFFFu);
+      atomicAdd(&s.part[kThreads + at_i / own], (uint32_t)(w >> 20));
+    }
+    __syncthreads();
+    sum += s.part[tid] + ((u64)s.part[kThreads + tid] << 20);
+  } else {
 #pragma unroll 4
-  for (int i = t0; i < t1; ++i) {
-    const float x = at(i);
-    if (x >= cut && bin64(x, whole) >= sure_to) {
-      sum += kept_weight(x, tr);
-      if (x == cut) ++tr;
+    for (int i = t0; i < t1; ++i) {
+      const float x = at(i);
+      if (x >= cut && bin64(x, whole) >= sure_to) {
+        sum += kept_weight(x, tr);
+        if (x == cut) ++tr;
+      }
     }
   }
   u64 mine_all;
