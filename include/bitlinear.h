@@ -304,8 +304,9 @@ BL_API int bitlinear_forward_blocks_bf16(const uint16_t* x, int64_t M, int64_t N
  * K % 16 == 0; a row has G = ceil(K / group) scales, the last group may be
  * short. x is fp32 or bf16 and is not quantised; S is fp32 or bf16; y is fp32.
  * The codes and their products with x are exact (an fp32 x takes part as its
- * three 8-bit significand pieces), the sums are held in fp32, and the scale is
- * applied to a group's sum. A non-finite x[m,k] reaches y[m,:] only.
+ * three 8-bit significand pieces; bits of it below 2^-133, which |x| < 2^-110
+ * has, are left out), the sums are held in fp32, and the scale is applied to a
+ * group's sum. A non-finite x[m,k] reaches y[m,:] only.
  *
  * `packed` is one opaque buffer of bitlinear_w4_packed_bytes() bytes (16-byte
  * aligned), laid out once per weight: 16-row tiles, each a run of 128-column
@@ -351,8 +352,11 @@ BL_API int bitlinear_w4_export(const void* packed, int64_t N, int64_t K, int gro
 BL_API size_t bitlinear_w4_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* y [M, N] fp32 from x [M, K] fp32 and a packed 4-bit weight. All pointers
- * 16-byte aligned, ws 256-byte aligned. Calls that can overlap need a
- * workspace each. bitlinear_workspace_error() reads ws. Asynchronous. */
+ * 16-byte aligned, ws 256-byte aligned. Calls that can overlap (captured ones
+ * among them) need a workspace each: it holds the error word, the pieces of an
+ * fp32 x and partial sums of many tokens. x as bf16 columns, three per token for
+ * fp32: up to 16 columns stream the weights through mma.sync, more take tcgen05.
+ * bitlinear_workspace_error() reads ws. Asynchronous. */
 BL_API int bitlinear_forward_w4(const float* x, int64_t M, int64_t N, int64_t K, int group, int scale_type,
                                 const void* packed, float* y, void* ws, size_t ws_bytes, bl_stream_t stream);
 
