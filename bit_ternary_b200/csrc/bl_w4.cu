@@ -309,10 +309,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int xstride = p.blocks * kW4Cols * 2 + kStreamPadBytes;
-  // [warp][slot][row][col]: slot 0 a tile that an earlier warp began, 1 a tile
-  // that a later warp ends, 2 a whole tile.
+  // [warp][slot][row][col]: slot 0 a tile that an earlier warp began, 1 a whole
+  // tile or, at the end, one that a later warp ends.
   float* part = reinterpret_cast<float*>(smem);
-  uint8_t* xs = smem + 3 * kStreamWarps * kPart * 4;
+  uint8_t* xs = smem + 2 * kStreamWarps * kPart * 4;
 
   const int64_t tile0 = p.tiles * blockIdx.x / gridDim.x, tile1 = p.tiles * (blockIdx.x + 1) / gridDim.x;
   const int64_t run = (tile1 - tile0) * p.blocks;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
       for (int i = 0; i < 4; ++i) tot[nt][i] = 0.f;
   };
   const auto store_part = [&](int slot) {
-    float* mine = part + (warp * 3 + slot) * kPart;
+    float* mine = part + (warp * 2 + slot) * kPart;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       *reinterpret_cast<float2*>(mine + g * kPartStride + 8 * nt + 2 * t) = make_float2(tot[nt][0], tot[nt][1]);
@@ -412,15 +412,17 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
   const auto write_tile = [&](int64_t tile, int slot, int64_t end) {
     constexpr int kMine = kW4Rows * kCols / 32;  // columns of a lane, every second one
     const int row = lane & (kW4Rows - 1), col0 = lane / kW4Rows;
-    const float* from = part + (warp * 3 + slot) * kPart + row * kPartStride + col0;
+    float* mine = part + (warp * 2 + slot) * kPart + row * kPartStride;
     float v[kMine];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) v[i] = from[2 * i];
+    for (int i = 0; i < kMine; ++i)
+      if (2 * i < p.cols) v[i] = mine[col0 + 2 * i];
     for (int w = warp + 1; w < kStreamWarps && warp_begin(w) < end; ++w) {
       if (warp_begin(w) == warp_begin(w + 1)) continue;
-      const float* q = part + w * 3 * kPart + row * kPartStride + col0;
+      const float* q = part + w * 2 * kPart + row * kPartStride + col0;
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) v[i] += q[2 * i];
+      for (int i = 0; i < kMine; ++i)
+        if (2 * i < p.cols) v[i] += q[2 * i];
     }
     const int64_t n = tile * kW4Rows + row;
     if (kBf16X) {
@@ -428,9 +430,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
       for (int i = 0; i < kMine; ++i)
         if (col0 + 2 * i < p.M && n < p.N) p.y[(int64_t)(col0 + 2 * i) * p.N + n] = v[i] * kW4Unit;
     } else {  // the columns of a token's pieces meet in this warp's slot
-      float* mine = part + (warp * 3 + slot) * kPart + row * kPartStride;
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) mine[col0 + 2 * i] = v[i];
+      for (int i = 0; i < kMine; ++i)
+        if (2 * i < p.cols) mine[col0 + 2 * i] = v[i];
       __syncwarp();
       for (int m = col0; m < p.M; m += 2)
         if (n < p.N) p.y[(int64_t)m * p.N + n] = (mine[m] + (mine[m + p.M] + mine[m + 2 * p.M])) * kW4Unit;
@@ -451,10 +453,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
         stream_block<NT, GPB, kBf16S>(ring[i], xb, xk, tot);
         xk += kW4Cols * 2;
         if (xk == xend) {
-          store_part(head ? 0 : 2);
+          store_part(head ? 0 : 1);
           if (!head) {
             __syncwarp();
-            write_tile(tile, 2, 0);
+            write_tile(tile, 1, 0);
             __syncwarp();
           }
           clear();
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
 }
 
 size_t w4_stream_smem(int NT, int64_t cols, const W4Shape& sh) {
-  return (size_t)3 * kStreamWarps * kW4Rows * (8 * NT + 2) * 4 +
+  return (size_t)2 * kStreamWarps * kW4Rows * (8 * NT + 2) * 4 +
          (size_t)(cols + 1) * ((size_t)sh.blocks() * kW4Cols * 2 + kStreamPadBytes);
 }
 
