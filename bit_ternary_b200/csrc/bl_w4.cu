@@ -161,8 +161,8 @@ __global__ void __launch_bounds__(256) w4_export_kernel(const uint8_t* __restric
 // 47 cycles a block, and its integer pipe takes 2 cycles per warp instruction:
 // what is not unpacking is kept off it (columns past the last token read a row
 // of zeros instead of being masked, products start from a zero register).
-// Measured, one bf16 token: 128000 x 2560 35 us (169 MB, 4.8 TB/s, 75% of a
-// copy's rate); 13824 x 2560, groups of 32, 6.9 us a launch in a graph (20 MB).
+// Measured in a graph, one bf16 token: 128000 x 2560 32.9 us (169 MB, 5.2 TB/s,
+// 80% of a copy's rate); 13824 x 2560, groups of 32, 6.8 us (20 MB).
 constexpr int kStreamWarps = 8;
 constexpr int kStreamPadBytes = 64;  // column stride = 64 mod 128: no bank conflicts between columns
 constexpr size_t kStreamSmemMax = 225 * 1024;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
   // (an empty run, of a CTA with fewer blocks than warps, holds nothing). Row
   // fastest, so 16 neighbouring y are written together. A lane's sums are added
   // side by side, warp after warp: one after the other, 16 tokens through 2560 x
-  // 2560 took 10.9 us instead of 5.5.
+  // 2560 took 10.9 us instead of 6.5.
   const auto write_tile = [&](int64_t tile, int slot, int64_t end) {
     constexpr int kMine = kW4Rows * kCols / 32;  // columns of a lane, every second one
     const int row = lane & (kW4Rows - 1), col0 = lane / kW4Rows;
