@@ -353,7 +353,9 @@ class W4Weights:
 
 def _w4_packed_bytes(N: int, K: int, group: int, scale_dtype: torch.dtype) -> int:
     L = _lib.lib()
-    if int(L.bitlinear_w4_groups(K, group)) <= 0 or not 0 <= N < 1 << 31:
+    # Compared here first: ctypes would take a size past its C type modulo 2^32 or 2^64.
+    if (group not in (32, 64, 128) or not 0 <= N < 1 << 31 or not 0 < K < 1 << 31
+            or int(L.bitlinear_w4_groups(K, group)) <= 0):
         raise ValueError(f"invalid N = {N}, K = {K} or group = {group} (K % 16 == 0, group 32, 64 or 128)")
     return int(L.bitlinear_w4_packed_bytes(N, K, group, _W4_SCALES[scale_dtype]))
 
