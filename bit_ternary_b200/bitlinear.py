@@ -323,6 +323,16 @@ def _same_device(t: torch.Tensor, name: str, device: torch.device) -> None:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _workspace(ws: torch.Tensor, device: torch.device) -> int:
+    """Bytes of a caller's workspace. An expanded or strided tensor has more
+    elements than bytes behind its pointer."""
+    if ws.device != device:
+        _same_device(ws, "ws", device)
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.numel()
+
+
 class W4Weights:
     """A weight [N, K] of 4-bit codes with a scale per `group` columns of a row
     (scale_dtype fp32 or bf16), in the library's packed layout."""
@@ -374,9 +384,8 @@ def pack_weights_w4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
     data = torch.empty(_w4_packed_bytes(N, K, group, scale_dtype), dtype=torch.uint8, device=W.device)
     if ws is None:
         ws = _alloc_ws(_lib.lib().bitlinear_pack_workspace_size(N, K), W.device)
-    _same_device(ws, "ws", W.device)
     _call_on(W.device, "bitlinear_pack_weights_w4" + sfx, W.data_ptr(), N, K, group, _W4_SCALES[scale_dtype],
-             data.data_ptr(), ws.data_ptr(), ws.numel())
+             data.data_ptr(), ws.data_ptr(), _workspace(ws, W.device))
     return W4Weights(data, N, K, group, scale_dtype)
 
 
@@ -444,10 +453,8 @@ def forward_w4(x: torch.Tensor, w: W4Weights, out: Optional[torch.Tensor] = None
             raise ValueError(f"out must have shape [{M}, {N}], got {list(y.shape)}")
     if ws is None:
         ws = _alloc_ws(w4_workspace_size(M, N, K), device)
-    else:
-        _same_device(ws, "ws", device)
     _call_on(device, "bitlinear_forward_w4" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type,
-             w._data.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel())
+             w._data.data_ptr(), y.data_ptr(), ws.data_ptr(), _workspace(ws, device))
     return y
 
 
@@ -523,9 +530,9 @@ def forward_w4_sample(x: torch.Tensor, w: W4Weights, u: torch.Tensor, temperatur
     logprobs = torch.empty(M, dtype=torch.float32, device=device)
     if ws is None:
         ws = _alloc_ws(w4_sample_workspace_size(M, N, K), device)
-    _same_device(ws, "ws", device)
     _call_on(device, "bitlinear_forward_w4_sample" + sfx, x.data_ptr(), M, N, K, w.group, w.scale_type,
-             w._data.data_ptr(), how, u_ptr, tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), ws.numel())
+             w._data.data_ptr(), how, u_ptr, tokens.data_ptr(), logprobs.data_ptr(), ws.data_ptr(),
+             _workspace(ws, device))
     return tokens, logprobs
 
 

@@ -1,6 +1,7 @@
-"""CPU tests of the binding's checks of 4-bit weights: sizes that a C type would
+"""The binding's checks of 4-bit weights: sizes that a C type would
 take modulo 2^32 or 2^64 (the kernels would then index with another layout than
-the tensors have) are refused before any launch."""
+the tensors have) and workspaces with fewer bytes than elements are refused
+before any launch."""
 import pytest
 
 from bit_ternary_b200 import build
@@ -35,3 +36,25 @@ def test_packed_bytes(B, dtype, scale_bytes):
         tiles, blocks = -(-N // 16), -(-K // 128)
         assert B._w4_packed_bytes(N, K, group, dtype) == tiles * blocks * (1024 + 16 * (128 // group) * scale_bytes)
     assert B._w4_packed_bytes(0, 128, 32, dtype) == 0
+
+
+def test_a_workspace_is_as_large_as_it_says(B):
+    """One byte expanded to a size, or every second byte, is not that many bytes."""
+    cpu = torch.device("cpu")
+    assert B._workspace(torch.zeros(512, dtype=torch.uint8), cpu) == 512
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(512), torch.zeros(1024, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            B._workspace(ws, cpu)
+    with pytest.raises(ValueError):
+        B._workspace(torch.zeros(512, dtype=torch.uint8), torch.device("cuda:0"))
+
+
+@pytest.mark.gpu
+def test_calls_refuse_a_workspace_that_is_smaller_than_it_says(B):
+    W, x, u = torch.randn(32, 64, device="cuda"), torch.randn(2, 64, device="cuda"), torch.rand(2, device="cuda")
+    w = B.pack_weights_w4(W, 32)
+    ws = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20)
+    for call in (lambda: B.pack_weights_w4(W, 32, ws=ws), lambda: B.forward_w4(x, w, ws=ws),
+                 lambda: B.forward_w4_sample(x, w, u, ws=ws)):
+        with pytest.raises(ValueError):
+            call()
