@@ -351,6 +351,12 @@ class W4Weights:
         self.scale_dtype = scale_dtype
         self.scale_type = _W4_SCALES[scale_dtype]
 
+    def __setattr__(self, name: str, value) -> None:
+        # The launches take the sizes as they stand here, so they stay with the bytes that were checked.
+        if name in self.__dict__:
+            raise AttributeError(f"{name} is fixed: another layout needs another W4Weights")
+        object.__setattr__(self, name, value)
+
     @property
     def data(self) -> torch.Tensor:
         """The packed bytes (another tensor needs another W4Weights, which checks it)."""

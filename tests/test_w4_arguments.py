@@ -58,3 +58,17 @@ def test_calls_refuse_a_workspace_that_is_smaller_than_it_says(B):
                  lambda: B.forward_w4_sample(x, w, u, ws=ws)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_weight_keeps_the_sizes_it_was_laid_out_for(B):
+    """Sizes that do not belong to the packed bytes would be read past their end."""
+    w = B.W4Weights.__new__(B.W4Weights)
+    names = ("out_features", "in_features", "group", "scale_dtype", "scale_type")
+    for name in names:
+        setattr(w, name, 1)
+    for name in names:
+        with pytest.raises(AttributeError):
+            setattr(w, name, 2)
+        assert getattr(w, name) == 1
+    with pytest.raises(AttributeError):
+        w.data = torch.zeros(16, dtype=torch.uint8)
