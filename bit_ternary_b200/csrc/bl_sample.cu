@@ -22,6 +22,7 @@
 // Measured, fp32 logits: 1 x 128000, top-k and top-p, 16.6 us; 32 x 32000 without
 // filters 11 us; 256 x 128000 with top-p 278 us (131 MB: a copy's rate is 20 us).
 #include "bl_internal.h"
+#include "bl_sample_bounds.h"
 
 #include <cstddef>
 
@@ -697,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   // key from the top, kDigits values each: weights added up per value, the value
   // that holds the border, then its keys alone (two rounds for most rows; a sort of
   // 800 candidates in all CTAs took a quarter of a row's time, 21000 of 85000 cycles).
+  // False, and nothing settled, where the list does not hold the border.
   const auto settle = [&](int m, u64 need, bool by_weight) {
     constexpr int kE = kListMax / kThreads;
     uint32_t key[kE];
@@ -743,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       const u64 mine = tid < kDigits ? s.digit[tid] + ((u64)s.digit[kDigits + tid] << 20) : 0ull;
       u64 all;
       const u64 run = block_scan<kThreads>(mine, s, all);
+      if (need - 1ull >= all) return false;  // none, or more than the list weighs
       if (run < need && run + mine >= need) {
         const uint32_t top = hk - ((uint32_t)tid << sh), span = (1u << sh) - 1u;
         s.hi_key = top;
@@ -763,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     ties = (need + each - 1) / each;
     partial = ties * each < weight_all;
     __syncthreads();
+    return true;
   };
   // The border without a list (more equal or near tokens than one holds):
   // bisection over the keys, a pass each. All CTAs take part and agree.
@@ -842,21 +846,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
     __syncthreads();
   };
-  // The bins in which a running weight meets a target, by bounds of every
-  // bin's weight: a token f bins past the bin's start weighs e^(-delta f) of it,
-  // between 1 - delta f and the chord; f is known to half a step of the
-  // histogram's sums and the rounding of the bin position (three of 2^-24 of 2047 bins, under 0.002). `first` is the weight at the bins' origin. The target is
-  // share * total (target < 0) or a weight. In fp32, whose errors over 2048
-  // additions stay below the 2e-5 that the borders are widened by.
+  // The bins in which a running weight meets a target, by bounds of every bin's
+  // weight (bin_weight). `first` is the weight at the bins' origin. The target is
+  // share * total (target < 0) or a weight. In fp32: the exponent (up to 29) has
+  // three roundings and expf two ulp, under 6e-6, a bound's own arithmetic, the
+  // additions of a prefix (14 deep) and the comparison under 2e-6; the borders are
+  // widened by 2e-5 on either side.
   const auto place_weight = [&](const Bins& g, float first, float target, bool may_whole, bool open_end) {
     // Exponent per bin (no bins to speak of where all tokens are equal or T is infinite).
     const float inv_tf = (float)inv_t;
     const float delta = g.scale < INFINITY && inv_tf > 0.0f ? fminf(inv_tf / g.scale, 1.0f) : 0.0f;
-    // The mean place of a word's step and how far from it a token may be, in bins.
-    const float unit = packed == 19 ? 1.0f / 64.0f : (packed == 18 ? 1.0f / 16.0f : 0.0f);
-    const float mid = packed == 19 ? 0.0f : (packed == 18 ? 1.5f / 64.0f : 0.5f);
-    const float fe = (packed == 19 ? 0.5f / 64.0f : (packed == 18 ? 2.0f / 64.0f : 0.5f)) + 0.002f;
-    const float shrink = delta * (1.0f - delta * (0.5f - delta * (1.0f / 6.0f)));
+    const BinPlaces places = bin_places(packed);
     const float step = expf(-delta);
     float e = first * expf(-delta * (float)(tid * kPerThread));
     float lo[kPerThread], hi[kPerThread], slo = 0.f, shi = 0.f;
@@ -866,10 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     for (int j = 0; j < kPerThread; ++j) {
       const int bin = tid * kPerThread + j;
       cnt += mine[j] = s.cnt[bin];
-      const float c = (float)mine[j], f = (float)s.off[bin] * unit + c * mid;
-      const float slack = c * 1e-12f;  // the rounding to 2^-40
-      lo[j] = c > 0.f ? fmaxf(e * (c - delta * (f + c * fe)) - slack, 0.f) : 0.f;
-      hi[j] = c > 0.f ? e * (c - shrink * fmaxf(f - c * fe, 0.f)) * (1.0f + delta * delta) + slack : 0.f;
+      const WeightBounds w = bin_weight(e, delta, places, mine[j], s.off[bin]);
+      lo[j] = w.lo;
+      hi[j] = w.hi;
       if ((open_end && bin == kBins - 1) || (uint32_t)bin == cut_bin) lo[j] = 0.f;
       slo += lo[j];
       shi += hi[j];
@@ -989,11 +988,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       }
       if (list) v.c = flush(C);
       v = cluster_sum(v);
+      if (by_weight && v.b >= need) return false;
       need = by_weight ? need - v.b : in_bin;
-      if (list) {
-        settle((int)v.c, need, by_weight);
-        return true;
-      }
+      if (list) return settle((int)v.c, need, by_weight);
       if (nlk == lk && nhk == hk) break;
       lk = nlk;
       hk = nhk;
@@ -1102,16 +1099,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       if (rank == 0) draw_from_list((int)v.c, by_k ? kset : kListMax, true, false, total);
       return;
     }
-    if (mode == kBorder) {
-      settle((int)v.c, need - v.b, true);
-      if (!partial) listed = (int)v.c;
-    } else {
+    bool settled = v.b < need;
+    if (settled && mode == kBorder) {
+      settled = settle((int)v.c, need - v.b, true);
+      if (settled && !partial) listed = (int)v.c;
+    } else if (settled) {
       bin_range(whole, 1u, 0xFFFFFFFFu);
-      if (!zoom(need - v.b, true, s.lo_key, s.hi_key, count)) {
-        bisect(need, true);
-        sure = 0;
-        sure_to = 0u;
-      }
+      settled = zoom(need - v.b, true, s.lo_key, s.hi_key, count);
+    }
+    if (!settled) {
+      bisect(need, true);
+      sure = 0;
+      sure_to = 0u;
     }
   }
 
