@@ -856,6 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     // Exponent per bin (no bins to speak of where all tokens are equal or T is infinite).
     const float inv_tf = (float)inv_t;
     const float delta = g.scale < INFINITY && inv_tf > 0.0f ? fminf(inv_tf / g.scale, 1.0f) : 0.0f;
+    // T and the span so large that their bins' range is infinite: the first bin and
+    // the last hold tokens at any distance, and a bin's weight is between none and all.
+    const bool blind = !(g.scale > 0.0f);
     const BinPlaces places = bin_places(packed);
     const float step = expf(-delta);
     float e = first * expf(-delta * (float)(tid * kPerThread));
@@ -867,8 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       const int bin = tid * kPerThread + j;
       cnt += mine[j] = s.cnt[bin];
       const WeightBounds w = bin_weight(e, delta, places, mine[j], s.off[bin]);
-      lo[j] = w.lo;
-      hi[j] = w.hi;
+      lo[j] = blind ? 0.f : w.lo;
+      hi[j] = blind ? first * (float)mine[j] : w.hi;
       if ((open_end && bin == kBins - 1) || (uint32_t)bin == cut_bin) lo[j] = 0.f;
       slo += lo[j];
       shi += hi[j];
