@@ -23,8 +23,10 @@
 // filters 11 us; 256 x 128000 with top-p 278 us (131 MB: a copy's rate is 20 us).
 #include "bl_internal.h"
 #include "bl_sample_bounds.h"
+#include "bl_sample_cut.h"
 
 #include <cstddef>
+#include <type_traits>
 
 namespace bl {
 
@@ -35,9 +37,6 @@ constexpr int kBins = 2048;          // the last one holds what lies past the ra
 constexpr int kListMax = 1024;       // tokens that a list of candidates holds
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;  // of a key, where a border is sought among candidates
 constexpr int kWholeMax = 512;       // up to this many the draw itself runs from the list (a sort in registers)
-constexpr int kMaxCluster = 16;
-constexpr int kPackMax = 16383;      // tokens per CTA whose count and places fit 14 + 18 bits
-constexpr size_t kSampleSmemMax = 225 * 1024;
 constexpr double kWeightOne = 1099511627776.0;  // 2^40
 constexpr double kTail = 29.0;       // exp(-29) * 2^40 rounds to zero
 
@@ -1190,37 +1189,81 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   }
 }
 
-template <int kThreads, bool kBf16, bool kResident>
-cudaError_t launch_sample_t(const SampleParams& p, int64_t B, int C, size_t smem, cudaStream_t stream) {
-  static std::atomic<uint64_t> allowed{0};
-  auto kern = sample_kernel<kThreads, kBf16, kResident>;
-  const cudaError_t e = allow_smem(kern, kSampleSmemMax, allowed, true);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(B * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
+// A launch of B rows, C CTAs each.
+struct Launch {
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  cudaLaunchConfig_t cfg = {};  // points at attr
+  Launch(const Launch&) = delete;
+  Launch(int64_t B, int C, int threads, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3((unsigned)(B * C));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+template <int kThreads, bool kBf16, bool kResident>
+cudaError_t allow_sample() {
+  static std::atomic<uint64_t> allowed{0};
+  return allow_smem(sample_kernel<kThreads, kBf16, kResident>, kSampleSmemMax, allowed, true);
 }
 
-}  // namespace
+template <int kThreads, bool kBf16, bool kResident>
+cudaError_t launch_sample_t(const SampleParams& p, int64_t B, int C, size_t smem, cudaStream_t stream) {
+  const cudaError_t e = allow_sample<kThreads, kBf16, kResident>();
+  if (e != cudaSuccess) return e;
+  const Launch l(B, C, kThreads, smem, stream);
+  return cudaLaunchKernelEx(&l.cfg, sample_kernel<kThreads, kBf16, kResident>, p);
+}
 
-cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, int64_t ld, const SampleHow& how,
-                          const float* u, int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms) {
-  // CTAs per row: so many that a stretch packs its histogram and two CTAs fit
-  // an SM, then more while rows alone leave SMs idle and stretches stay long.
-  int C = 1;
-  while (C < kMaxCluster && ((V + C - 1) / C > kPackMax || (B * C * 2 <= 2 * num_sms && V / (2 * C) >= 2048))) C *= 2;
+// Whether the device can run a cluster of kMaxCluster CTAs of this form. It needs as
+// many free SMs in one part of the chip, which no size of cluster above
+// kPortableCluster is sure of. Asked once per device, at the largest shared memory.
+template <int kThreads, bool kBf16, bool kResident>
+bool largest_cluster_fits() {
+  static std::atomic<uint64_t> asked{0}, yes{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((asked.load(std::memory_order_acquire) & bit) == 0) {
+    int n = 0;
+    const Launch l(1, kMaxCluster, kThreads, kSampleSmemMax, nullptr);
+    if (allow_sample<kThreads, kBf16, kResident>() == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, sample_kernel<kThreads, kBf16, kResident>, &l.cfg) == cudaSuccess && n > 0)
+      yes.fetch_or(bit, std::memory_order_relaxed);
+    else
+      cudaGetLastError();  // an answer, not an error of the call
+    asked.fetch_or(bit, std::memory_order_release);
+  }
+  return (yes.load(std::memory_order_relaxed) & bit) != 0;
+}
+
+// One of the six kernel forms: f(threads, bf16, resident) with each as a constant.
+template <bool kBf16, typename F>
+auto with_form(const SampleCut& c, F f) {
+  using std::integral_constant;
+  using Bf16 = integral_constant<bool, kBf16>;
+  if (!c.resident) return f(integral_constant<int, 512>(), Bf16(), std::false_type());
+  if (c.wide) return f(integral_constant<int, 1024>(), Bf16(), std::true_type());
+  return f(integral_constant<int, 512>(), Bf16(), std::true_type());
+}
+
+template <bool kBf16>
+cudaError_t launch_sample_x(const void* logits, int64_t B, int64_t V, int64_t ld, const SampleHow& how, const float* u,
+                            int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms) {
+  const SampleCut c = sample_cut(B, V, num_sms, sizeof(Smem), [](const SampleCut& s) {
+    return with_form<kBf16>(s, [](auto threads, auto bf16, auto resident) {
+      return largest_cluster_fits<decltype(threads)::value, decltype(bf16)::value, decltype(resident)::value>();
+    });
+  });
   SampleParams p;
   p.logits = logits;
   p.how = how;
@@ -1229,17 +1272,14 @@ cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, i
   p.logprobs = logprobs;
   p.V = V;
   p.ld = ld;
-  p.per = (int)((V + C - 1) / C);
-  p.cluster = C;
-  const size_t need = sizeof(Smem) + 4 * (size_t)(p.per + 16);
-  const bool resident = need <= kSampleSmemMax;
-  const size_t smem = resident ? need : sizeof(Smem);
+  p.per = c.per;
+  p.cluster = c.cluster;
   // A launch takes fewer than 2^31 CTAs: long batches go in parts.
-  const int64_t rows = 0x7FFFFFFF / C;
+  const int64_t rows = 0x7FFFFFFF / c.cluster;
   for (int64_t b = 0; b < B; b += rows) {
     SampleParams q = p;
     const int64_t part = B - b < rows ? B - b : rows;
-    q.logits = static_cast<const char*>(logits) + b * ld * (bf16 ? 2 : 4);
+    q.logits = static_cast<const char*>(logits) + b * ld * (kBf16 ? 2 : 4);
     if (how.temperature != nullptr) q.how.temperature += b;
     if (how.top_k != nullptr) q.how.top_k += b;
     if (how.top_p != nullptr) q.how.top_p += b;
@@ -1247,20 +1287,21 @@ cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, i
     q.u += b;
     q.tokens += b;
     if (logprobs != nullptr) q.logprobs += b;
-    // A launch that gives every SM one CTA at most takes the wide ones.
-    const bool wide = part * C <= num_sms;
-    cudaError_t e;
-    if (bf16)
-      e = !resident ? launch_sample_t<512, true, false>(q, part, C, smem, stream)
-          : wide    ? launch_sample_t<1024, true, true>(q, part, C, smem, stream)
-                    : launch_sample_t<512, true, true>(q, part, C, smem, stream);
-    else
-      e = !resident ? launch_sample_t<512, false, false>(q, part, C, smem, stream)
-          : wide    ? launch_sample_t<1024, false, true>(q, part, C, smem, stream)
-                    : launch_sample_t<512, false, true>(q, part, C, smem, stream);
+    const cudaError_t e = with_form<kBf16>(c, [&](auto threads, auto bf16, auto resident) {
+      return launch_sample_t<decltype(threads)::value, decltype(bf16)::value, decltype(resident)::value>(
+          q, part, c.cluster, c.smem, stream);
+    });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const void* logits, bool bf16, int64_t B, int64_t V, int64_t ld, const SampleHow& how,
+                          const float* u, int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms) {
+  return bf16 ? launch_sample_x<true>(logits, B, V, ld, how, u, tokens, logprobs, stream, num_sms)
+              : launch_sample_x<false>(logits, B, V, ld, how, u, tokens, logprobs, stream, num_sms);
 }
 
 }  // namespace bl
