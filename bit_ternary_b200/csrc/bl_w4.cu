@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<NT>()) w4_strea
   // (an empty run, of a CTA with fewer blocks than warps, holds nothing). Row
   // fastest, so 16 neighbouring y are written together. A lane's sums are added
   // side by side, warp after warp: one after the other, 16 tokens through 2560 x
-  // 2560 took 10.9 us instead of 6.5.
+  // 2560 took 10.9 us instead of 6.5 (two CTAs an SM).
   const auto write_tile = [&](int64_t tile, int slot, int64_t end) {
     constexpr int kMine = kW4Rows * kCols / 32;  // columns of a lane, every second one
     const int row = lane & (kW4Rows - 1), col0 = lane / kW4Rows;
@@ -528,7 +528,11 @@ cudaError_t launch_w4_stream(const void* x, bool bf16, int64_t M, const W4Shape&
   const int NT = p.cols <= 8 ? 1 : 2;
   const size_t smem = w4_stream_smem(NT, p.cols, sh);
   int64_t per_sm = (227 * 1024) / (int64_t)(smem + 1024);
-  const int most = NT == 1 ? stream_ctas<1>() : stream_ctas<2>();
+  // 9 to 16 columns: a second CTA on an SM stages x a second time, which pays only
+  // where the SM has more than four tiles to stream (16 bf16 tokens through 2560
+  // columns, one CTA against two: 160 tiles 5.6 / 6.5 us, 600 9.0 / 9.5, 864 10.1 /
+  // 9.6, 8000 65 / 47; three weights in turn in a graph).
+  const int most = NT == 1 ? stream_ctas<1>() : (p.tiles > 4 * (int64_t)num_sms ? stream_ctas<2>() : 1);
   per_sm = per_sm < 1 ? 1 : (per_sm > most ? most : per_sm);
   const int64_t slots = num_sms * per_sm;
   const int grid = (int)(p.tiles < slots ? p.tiles : slots);
