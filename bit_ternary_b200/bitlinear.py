@@ -345,6 +345,7 @@ class W4Weights:
         if data.numel() != need:
             raise ValueError(f"data must hold {need} bytes")
         self._data = data
+        self.device = data.device
         self.out_features = N
         self.in_features = K
         self.group = group
@@ -353,7 +354,7 @@ class W4Weights:
 
     def __setattr__(self, name: str, value) -> None:
         # The launches take the sizes as they stand here, so they stay with the bytes that were checked.
-        if name in self.__dict__:
+        if hasattr(self, name):
             raise AttributeError(f"{name} is fixed: another layout needs another W4Weights")
         object.__setattr__(self, name, value)
 
@@ -361,10 +362,6 @@ class W4Weights:
     def data(self) -> torch.Tensor:
         """The packed bytes (another tensor needs another W4Weights, which checks it)."""
         return self._data
-
-    @property
-    def device(self) -> torch.device:
-        return self._data.device
 
 
 def _w4_packed_bytes(N: int, K: int, group: int, scale_dtype: torch.dtype) -> int:
