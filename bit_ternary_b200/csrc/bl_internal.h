@@ -206,8 +206,8 @@ __device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&pair)[4]) {
 }
 // The one-launch kernel for few tokens (bl_w4.cu) holds x in shared memory as
 // bf16 columns: a token of bf16 x is one, a token of fp32 x three. Up to 16, two
-// matrix instructions a step: 16 bf16 tokens take 6.5 us through 2560 x 2560 and
-// 9.1 through 13824 x 2560, where the tensor-core kernel takes 7.9 and 11.8.
+// matrix instructions a step: 16 bf16 tokens take 5.6 us through 2560 x 2560 and
+// 9.1 through 13824 x 2560 (weights in L2), where the tensor-core kernel takes 7.9 and 11.8.
 constexpr int kW4StreamCols = 16;
 bool w4_stream_fits(int64_t M, bool bf16, const W4Shape& sh);
 // Most parts of K whose partial sums the workspace holds: none where tiles of 128

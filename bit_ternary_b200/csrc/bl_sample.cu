@@ -1,26 +1,34 @@
 // bl_sample.cu - one token per row of logits: temperature, top-k, top-p, min-p
 // and a draw by a given uniform number.
 //
-// Weights w = exp((x - max) / T) are rounded to multiples of 2^-40 and added as
-// 64-bit integers (V <= 2^22 keeps a row's sum below 2^62), so every sum is
-// exact and no order of adding changes the token.
+// Weights w = exp((x - max) / T) are whole multiples of 2^-40 (each within one of
+// the exact value) and added as 64-bit integers (V <= 2^22 keeps a row's sum below
+// 2^62), so every sum of them is exact and no order of adding changes the token.
 //
 // A cluster of 1 to 16 CTAs owns a row: each CTA reads its stretch once into
 // shared memory, and every later pass runs there. The thresholds of top-k and
 // top-p come from one histogram of 2048 bins, linear in x, of one 32-bit atomic
 // per token: a count and the sum of the tokens' places in the bin. Counts place
 // the k-th token in a bin exactly; the places bound every bin's weight to
-// about 0.05%, which places the border of top-p within a bin or two without an
-// exponential. The tokens of those bins (some hundreds) settle the
-// border exactly. Top-p then needs one exponential per token for the exact
-// sum, a draw without filters likewise, top-k none beyond the kept tokens.
+// about 0.05%, which places the border of top-p within a few bins without an
+// exponential. Where a list holds the tokens of those bins (1024; some hundreds at
+// p = 0.9 of 128000), they settle the border exactly; where it does not (p near 1 in
+// a broad row; more than 16 x 16383 = 262128 tokens, whose words have no room for
+// places and bound a bin's weight to about 1.4%), finer bins over their range come
+// first. Top-p then needs one exponential per token for the exact sum, a draw
+// without filters likewise, top-k none beyond the kept tokens.
 //
 // Few rows are bound by the chain of barriers (one over a cluster takes about
 // 1 us), so a row is spread over up to 16 CTAs and no CTA waits for another's
-// verdict; many rows by instructions (under top-p a token takes an exponential in
-// fp64, an atomic and its places), not by the single read of the logits.
-// Measured, fp32 logits: 1 x 128000, top-k and top-p, 16.6 us; 32 x 32000 without
-// filters 11 us; 256 x 128000 with top-p 278 us (131 MB: a copy's rate is 20 us).
+// verdict. Many rows are bound by latency too, not by the single read of the logits
+// and by no unit: in 256 x 128000 with top-p the schedulers issue 54% of the time
+// (ALU 39%, shared memory 36%, fp64 8%, DRAM 6%), and of 12 cycles that a warp takes
+// per instruction 2.4 are fixed latencies, 2.0 barriers, 1.4 shared memory: two CTAs
+// an SM (64 registers, 104 KB) cover one another's phases only in part.
+// Measured in a graph, fp32 logits: 1 x 128000, top-k and top-p, 16.5 us, top-p alone
+// 21.6; 32 x 32000 without filters 10.3; 256 x 128000 with p = 0.9 248, with p of
+// 0.8 to 0.99 by rows 277 to 286 (131 MB: a copy's rate is 20 us); 64 x 262128 187,
+// 64 x 262144 290. The 1024-thread bf16 form spills 36 bytes a thread at its 64 registers.
 #include "bl_internal.h"
 #include "bl_sample_bounds.h"
 #include "bl_sample_cut.h"

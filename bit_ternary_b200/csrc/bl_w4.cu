@@ -27,7 +27,9 @@ __device__ __forceinline__ int64_t w4_block_off(const W4Shape& sh, int64_t tile,
 }
 
 // One warp per row of a block: lane l owns the block's columns 4l .. 4l+3, so
-// 8, 16 or 32 neighbouring lanes hold a group. Bandwidth-bound (W is read once).
+// 8, 16 or 32 neighbouring lanes hold a group. W is read once, but a warp has one
+// load of 512 bytes in flight and divides 64-bit indexes for each: 128000 x 2560
+// fp32 929 us with the read of the status word, where its bytes take 229.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) w4_pack_kernel(const void* __restrict__ W, const W4Shape sh,
                                                       uint8_t* __restrict__ packed, uint32_t* status) {
@@ -83,6 +85,8 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const void* __restrict__ W
 
 // Natural nibbles [N, K/2] and scales [N, G] to the packed layout: one thread
 // per word of eight columns; the first word of a group also moves its scale.
+// Offline: 128000 x 2560 354 us (its bytes take 52), the export 342 (78); a 64-bit
+// division and four scattered bytes per thread.
 __global__ void __launch_bounds__(256) w4_import_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ S,
                                                         const W4Shape sh, uint8_t* __restrict__ packed) {
   const int64_t words = sh.blocks() * 16;
@@ -161,8 +165,12 @@ __global__ void __launch_bounds__(256) w4_export_kernel(const uint8_t* __restric
 // 47 cycles a block, and its integer pipe takes 2 cycles per warp instruction:
 // what is not unpacking is kept off it (columns past the last token read a row
 // of zeros instead of being masked, products start from a zero register).
-// Measured in a graph, one bf16 token: 128000 x 2560 32.9 us (169 MB, 5.2 TB/s,
-// 80% of a copy's rate); 13824 x 2560, groups of 32, 6.8 us (20 MB).
+// The ring takes all 80 registers of three CTAs an SM, and most forms with fp32 x or
+// fp32 scales pass them: 4 to 36 bytes a thread are spilled (groups of 32, fp32 scales).
+// Measured in a graph, weights taken in turn from more than L2 holds: one bf16 token,
+// 128000 x 2560 33.2 us (169 MB, 5.1 TB/s, 79% of a copy's rate), 13824 x 2560 6.8 us,
+// groups of 32 7.0 us (20 MB); 16 bf16 tokens, 2560 x 2560 5.9, 13824 x 2560 9.8,
+// 128000 x 2560 48.1 us.
 constexpr int kStreamWarps = 8;
 constexpr int kStreamPadBytes = 64;  // column stride = 64 mod 128: no bank conflicts between columns
 constexpr size_t kStreamSmemMax = 225 * 1024;

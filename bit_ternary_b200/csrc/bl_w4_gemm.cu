@@ -25,9 +25,10 @@
 // scheduler slots they share bound it: beside twelve busy warps an instruction of
 // the MMA issuer takes about 8 cycles, so its loop holds little but MMAs, and a
 // group of 32 columns (two MMAs, then a drain) costs twice one of 128.
-// Measured back to back, bf16 x, 13824 x 2560: 4096 tokens 246 us (1180 TFLOP/s,
-// 70% of cuBLAS's bf16 rate), with groups of 32 560 us; 1024 tokens, groups of
-// 64, 89 us. fp32 x, 2560 x 6912, 512 tokens: 50 us (1070 TFLOP/s of bf16 MMAs).
+// Measured back to back, bf16 x, 13824 x 2560: 4096 tokens 248 us at full clock (1170
+// TFLOP/s, 69% of cuBLAS's bf16 rate; 270 to 290 where the power cap holds the clock),
+// with groups of 32 564 us; 1024 tokens, groups of 64, 89 us. fp32 x, 2560 x 6912,
+// 512 tokens: 48 us (1130 TFLOP/s of bf16 MMAs).
 // Every barrier wait is bounded in time; a timeout sets a shared abort flag and
 // the workspace's error word, and all roles run out and exit.
 #include "bl_internal.h"

@@ -305,8 +305,9 @@ BL_API int bitlinear_forward_blocks_bf16(const uint16_t* x, int64_t M, int64_t N
  * short. x is fp32 or bf16 and is not quantised; S is fp32 or bf16; y is fp32.
  * The codes and their products with x are exact (an fp32 x takes part as its
  * three 8-bit significand pieces; bits of it below 2^-133, which |x| < 2^-110
- * has, are left out), the sums are held in fp32, and the scale is applied to a
- * group's sum. A non-finite x[m,k] reaches y[m,:] only.
+ * has, are left out), the sums are held in fp32 (a group's scaled one to 2^-144
+ * where it is that small), and the scale is applied to a group's sum. A
+ * non-finite x[m,k] reaches y[m,:] only.
  *
  * `packed` is one opaque buffer of bitlinear_w4_packed_bytes() bytes (16-byte
  * aligned), laid out once per weight: 16-row tiles, each a run of 128-column
@@ -390,8 +391,8 @@ typedef struct {
  *   The token is the first kept index, in ascending order, whose running sum
  *   of w exceeds u times the kept sum (u NaN or < 0 counts as 0, u >= 1 takes
  *   the last token of positive weight).
- * The sums run over w rounded to multiples of 2^-40, exactly, so the token does not
- * depend on any order of adding.
+ * The sums run over w as whole multiples of 2^-40, each within one of them of the
+ * exact value, and are exact, so the token does not depend on any order of adding.
  *   tokens    device int64 [B]: the index, or -1 where every token is out.
  *   logprobs  device fp32 [B] or NULL: ln(w / kept sum) of the token (0 for
  *             T not > 0, -inf for -1).
