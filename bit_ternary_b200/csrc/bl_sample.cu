@@ -1232,26 +1232,29 @@ cudaError_t launch_sample_t(const SampleParams& p, int64_t B, int C, size_t smem
   return cudaLaunchKernelEx(&l.cfg, sample_kernel<kThreads, kBf16, kResident>, p);
 }
 
-// Whether the device can run a cluster of kMaxCluster CTAs of this form. It needs as
-// many free SMs in one part of the chip, which no size of cluster above
-// kPortableCluster is sure of. Asked once per device, at the largest shared memory.
+// How many clusters of C CTAs of this form device dev (the current one) runs at a time;
+// 0 where it cannot say. Asked once per device, C, and CTAs that shared memory lets on
+// an SM.
 template <int kThreads, bool kBf16, bool kResident>
-bool largest_cluster_fits() {
-  static std::atomic<uint64_t> asked{0}, yes{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const uint64_t bit = 1ull << (dev & 63);
-  if ((asked.load(std::memory_order_acquire) & bit) == 0) {
-    int n = 0;
-    const Launch l(1, kMaxCluster, kThreads, kSampleSmemMax, nullptr);
-    if (allow_sample<kThreads, kBf16, kResident>() == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&n, sample_kernel<kThreads, kBf16, kResident>, &l.cfg) == cudaSuccess && n > 0)
-      yes.fetch_or(bit, std::memory_order_relaxed);
-    else
+int clusters_at_once(int dev, int C, size_t smem) {
+  static std::atomic<int> known[64][5][2];  // the answer + 1
+  constexpr size_t kTwo = 228 * 1024 / 2 - 1024;  // shared memory of a CTA that leaves room for a second one
+  const bool two = kThreads == 512 && smem <= kTwo;
+  int size = 0;
+  while ((1 << size) < C) ++size;
+  std::atomic<int>& mine = known[dev & 63][size][two];
+  int n = mine.load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    n = 0;
+    const Launch l(1, C, kThreads, two ? kTwo : kSampleSmemMax, nullptr);
+    if (allow_sample<kThreads, kBf16, kResident>() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, sample_kernel<kThreads, kBf16, kResident>, &l.cfg) != cudaSuccess) {
       cudaGetLastError();  // an answer, not an error of the call
-    asked.fetch_or(bit, std::memory_order_release);
+      n = 0;
+    }
+    mine.store(n + 1, std::memory_order_relaxed);
   }
-  return (yes.load(std::memory_order_relaxed) & bit) != 0;
+  return n;
 }
 
 // One of the six kernel forms: f(threads, bf16, resident) with each as a constant.
@@ -1267,9 +1270,13 @@ auto with_form(const SampleCut& c, F f) {
 template <bool kBf16>
 cudaError_t launch_sample_x(const void* logits, int64_t B, int64_t V, int64_t ld, const SampleHow& how, const float* u,
                             int64_t* tokens, float* logprobs, cudaStream_t stream, int num_sms) {
-  const SampleCut c = sample_cut(B, V, num_sms, sizeof(Smem), [](const SampleCut& s) {
-    return with_form<kBf16>(s, [](auto threads, auto bf16, auto resident) {
-      return largest_cluster_fits<decltype(threads)::value, decltype(bf16)::value, decltype(resident)::value>();
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const SampleCut c = sample_cut(B, V, num_sms, sizeof(Smem), [&](const SampleCut& s) {
+    return with_form<kBf16>(s, [&](auto threads, auto bf16, auto resident) {
+      return clusters_at_once<decltype(threads)::value, decltype(bf16)::value, decltype(resident)::value>(
+          dev, s.cluster, s.smem);
     });
   });
   SampleParams p;
