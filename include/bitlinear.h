@@ -325,9 +325,10 @@ BL_API size_t bitlinear_w4_packed_bytes(int64_t N, int64_t K, int group, int sca
 /* Quantise and pack: per group a = max|w|, S = RN(a / 7) (rounded once more
  * to bf16 for BL_SCALE_BF16), c = clamp(rint(RN(w / S)), -8, 7); S = 0 and
  * c = 0 where S rounds to zero.
- *   W       device fp32 [N, K], read only.
+ *   W       device fp32 [N, K], 16-byte aligned, read only.
  *   packed  device buffer, fully overwritten.
- *   ws      device scratch of ws_bytes >= bitlinear_pack_workspace_size().
+ *   ws      device scratch of ws_bytes >= bitlinear_pack_workspace_size(), 256-byte
+ *           aligned; its status word is cleared.
  * Synchronous (it reads back the status word). BL_ERR_NONFINITE if a group
  * holds Inf or NaN; that group is packed as zeros. N >= 1 is required. */
 BL_API int bitlinear_pack_weights_w4(const float* W, int64_t N, int64_t K, int group, int scale_type, void* packed,
@@ -340,12 +341,12 @@ BL_API int bitlinear_pack_weights_w4_bf16(const uint16_t* W, int64_t N, int64_t 
 
 /* Lay out codes that are 4 bits already: codes device uint8 [N, K/2], two to
  * a byte (column 2j in the low nibble of byte j), stored as c + 8; S device
- * [N, G] of scale_type. Asynchronous. */
+ * [N, G] of scale_type. All pointers 16-byte aligned. Asynchronous. */
 BL_API int bitlinear_w4_import(const uint8_t* codes, const void* S, int64_t N, int64_t K, int group, int scale_type,
                                void* packed, bl_stream_t stream);
 
 /* The inverse: codes device int8 [N, K] (the values c, one to a byte) and S
- * [N, G] of scale_type. Asynchronous. */
+ * [N, G] of scale_type. All pointers 16-byte aligned. Asynchronous. */
 BL_API int bitlinear_w4_export(const void* packed, int64_t N, int64_t K, int group, int scale_type, int8_t* codes,
                                void* S, bl_stream_t stream);
 
