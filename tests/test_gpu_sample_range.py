@@ -143,3 +143,18 @@ def test_one_row_and_many_of_a_large_vocabulary(B):
             if i % 8 == 0:
                 a, b = B.sample(one, ud[i:i + 1], 1.0, 0, p)
                 assert int(a) == t and float(b) == float(lp[i])
+
+
+# Row counts at which the cut changes: the most that run at once as clusters of 16 wide and
+# narrow CTAs, of 8 and of 4, and one more.
+@pytest.mark.parametrize("rows", [7, 8, 14, 15, 16, 33, 36])
+@pytest.mark.parametrize("V", [20000, 50021])
+def test_row_counts_at_which_the_cut_changes(B, V, rows):
+    x = np.stack([long_row(V, ("body", "ties", "flat", "masked")[r % 4], 5 + r) for r in range(rows)])
+    u = ((np.arange(rows) + 0.5) / rows).astype(np.float32)
+    xd, ud = torch.from_numpy(x).cuda(), torch.from_numpy(u).cuda()
+    for T, k, p, m in ((1.0, 0, 0.9, 0.0), (0.75, 50, 0.9, 0.0), (1.0, 0, 1.0, 0.0)):
+        tok, lp = B.sample(xd, ud, T, k, p, m)
+        for r in range(rows):
+            t, l = sample_row_int64(x[r], float(u[r]), T, k, float(np.float32(p)), m)
+            assert int(tok[r]) == t and close(float(lp[r]), l, V), (T, k, p, r)
